@@ -89,8 +89,17 @@ typedef enum spin_status {
 #define SPIN_STATUS_BAD_ACCEPTED 0x10u /* accepted outside [0, rows - 1] */
 #define SPIN_STATUS_TIMEOUT      0x20u /* a bounded wait inside a kernel gave up */
 #define SPIN_STATUS_BAD_RHO      0x40u /* budget override outside [0, 10000] */
+#define SPIN_STATUS_BAD_PARENT   0x80u /* spin_pages_fork: a parent that is not a request, or changes itself */
+#define SPIN_STATUS_BAD_REF      0x100u /* a page released more often than it is referenced */
+#define SPIN_STATUS_NO_PAGES     0x200u /* spin_pages_reserve: a request's pages did not fit in the pool */
 
-typedef enum spin_dtype { SPIN_DTYPE_F32 = 0, SPIN_DTYPE_BF16 = 1, SPIN_DTYPE_E4M3 = 2 } spin_dtype_t;
+/* F16 is a type of the KV-cache calls' queries, outputs and new keys and values only. */
+typedef enum spin_dtype {
+    SPIN_DTYPE_F32 = 0,
+    SPIN_DTYPE_BF16 = 1,
+    SPIN_DTYPE_E4M3 = 2,
+    SPIN_DTYPE_F16 = 3
+} spin_dtype_t;
 
 /* Predicted slot score: Eq. 1's max(V[i], D[q-i]) (default) or the additive reading
  * V[i] + D[q-i]. */
@@ -442,6 +451,143 @@ spin_status_t spin_update_ema_age(const spin_config* cfg, float* V, float* D, fl
  * predictions, an identity block list and the top-K slots (4 B per request, row and slot,
  * and more); the stacked calls need n_layers times this. */
 spin_status_t spin_workspace_size(const spin_config* cfg, int32_t rows, size_t* bytes);
+
+/* ------------------------------------------------------------------------------------------
+ * The KV cache behind the indexer: keys and values in 8 bits with a scale for every page and
+ * key/value head, the attention that reads it (over a request's whole context, or over the
+ * slots the indexer's top-K picked: the core attention of §2, Algorithm 1's consumer), the
+ * call that writes it, and the calls that manage its pages.  No formula of the paper: it
+ * leaves the core attention and the cache to the serving engine.
+ *
+ * Layouts (R = n_req, rows <= max_rows query rows per request, block = page = 64 slots):
+ *   k_pool, v_pool  e4m3 codes [n_pages][64][kv_heads][head_dim], 16-byte aligned
+ *   k_scale, v_scale float [n_pages][kv_heads]: value = code * scale, for every slot of the page
+ *   block_table     int32 [R][bt_stride]  logical block -> page, -1 = none
+ *   n_slots         int32 [R][rows]       slots each query row sees (0: none)
+ *   q, out          [R][rows][n_heads][head_dim] in dtype, 16-byte aligned; query heads
+ *                   g * n_heads/kv_heads ... share key/value head g
+ *   lse             float [R][rows][n_heads], natural log; may be NULL
+ *   topk_idx        int32 [R][rows][top_k] slot ids in any order, -1 = none; NULL: every slot
+ * ------------------------------------------------------------------------------------------ */
+typedef struct spin_kv_config {
+    int32_t n_req;        /* 1 .. 65535 */
+    int32_t max_slots;    /* 1 .. 2^24 */
+    int32_t max_rows;     /* 1 .. 8 query rows per request */
+    int32_t block;        /* 64 */
+    int32_t n_heads;      /* 1 .. 128 query heads */
+    int32_t kv_heads;     /* divides n_heads */
+    int32_t head_dim;     /* a multiple of 16, 16 .. 256 */
+    int32_t dtype;        /* of q, out, new_k and new_v: F32, BF16 or F16 */
+    float softmax_scale;  /* finite; multiplies q . k */
+    int32_t reserved;     /* 0 */
+} spin_kv_config;
+
+/* Attention over the cache, for 1 .. max_rows query rows per request (decoding, speculative
+ * verification):
+ *   set     = {i < n_slots[b][r]}, or the listed i of row r with 0 <= i < n_slots[b][r]
+ *   s_i     = softmax_scale * k_scale * (q . code_k(i))
+ *   out     = sum_i exp(s_i) v_scale code_v(i) / sum_i exp(s_i)      (over the set)
+ *   lse     = ln sum_i exp(s_i)
+ * A row with an empty set gets out = 0 and lse = -inf.  A slot listed twice counts twice.
+ * Cached values outside a row's set (NaN codes among them) do not reach its outputs; a NaN
+ * code inside it does.  Products are exact, and sums, softmax weights' sums and the running
+ * maximum are fp32; the weights enter their product with the values as one f16 term for
+ * BF16 and F16, as two (22 bits) for F32, and queries as one f16 term scaled by a power of two per
+ * row (BF16, F16) or two (F32).
+ *
+ * Checked on the device: n_slots outside [0, max_slots] (BAD_N, the row counts as empty), a
+ * list entry outside [-1, n_slots) (BAD_LIST) and a slot whose page is outside [0, n_pages)
+ * (BAD_PAGE): such slots are left out of the set.
+ *
+ * workspace: spin_kv_workspace_size bytes, 256-byte aligned, uninitialised; it must not be
+ * shared by calls that may run at the same time (two streams, two graphs replayed together). */
+spin_status_t spin_kv_workspace_size(const spin_kv_config* cfg, int32_t rows, int32_t top_k,
+                                     size_t* bytes);
+spin_status_t spin_kv_attend(const spin_kv_config* cfg, const void* q, const uint8_t* k_pool,
+                             const uint8_t* v_pool, const float* k_scale, const float* v_scale,
+                             int64_t n_pages, const int32_t* block_table, int64_t bt_stride,
+                             const int32_t* n_slots, int32_t rows, const int32_t* topk_idx,
+                             int32_t top_k, void* out, float* lse, void* workspace,
+                             size_t workspace_bytes, uint32_t* status, spin_stream_t stream);
+
+/* Append to the cache: request r's new tokens new_start[r] .. new_start[r+1]-1 of new_k and
+ * new_v ([n_tokens][kv_heads][head_dim] in dtype, 16-byte aligned) become its slots
+ * n_before[r], n_before[r]+1, ...  For every page the new slots fall in, and every head:
+ *   s_old   = 0 if the first new slot of the page is the page's slot 0, else its scale
+ *   s_new   = max(s_old, the smallest power of two s >= 2^-126 with max|x| <= 448 s over the
+ *             page's finite new values; 0 if they are all zero)
+ *   the page's earlier slots   code <- e4m3(code * s_old / s_new)  (unless s_new = s_old)
+ *   the new slots              code  = e4m3(x * (1 / s_new)), infinities saturated, NaN kept
+ * (quotients and products rounded to fp32; 0 where s_new < 2^-126) and the scale becomes s_new.  Scales only grow within a page, and a page's content does not
+ * depend on what was in it before its slot 0 was written.  With power-of-two scales both are
+ * exact up to the e4m3 rounding.  Slots behind the new ones are
+ * left as they are.  Requests must not share a page they append to (spin_pages_reserve).
+ * max_new: the largest count of new tokens of a request (sizes the launch).
+ * Checked on the device: new_start not ascending within [0, n_tokens], a count above max_new,
+ * n_before < 0 or past max_slots with the new ones (BAD_N, the request is skipped), a page
+ * outside [0, n_pages) (BAD_PAGE, that page is skipped). */
+spin_status_t spin_kv_append(const spin_kv_config* cfg, const void* new_k, const void* new_v,
+                             int64_t n_tokens, const int32_t* new_start, int32_t max_new,
+                             const int32_t* n_before, uint8_t* k_pool, uint8_t* v_pool,
+                             float* k_scale, float* v_scale, int64_t n_pages,
+                             const int32_t* block_table, int64_t bt_stride, uint32_t* status,
+                             spin_stream_t stream);
+
+/* Page management.  The state is the caller's: block_table int32 [n_req][bt_stride] (-1 = no
+ * page) and ref int32 [n_pages], the number of table entries that use each page (0 = free).
+ * Pools are any arrays indexed by page (this cache's, the indexer's keys and scales):
+ * n_pools <= 16 host descriptors, data 4-byte aligned, page_bytes a multiple of 4.  Results
+ * do not depend on the order in which threads run: fresh pages are the lowest free ones,
+ * handed to requests in order.  A table entry outside [-1, n_pages) is treated as -1
+ * (BAD_PAGE); releasing a page that has no reference leaves it at 0 (BAD_REF).
+ * n_req 1 .. 65535, n_pages 1 .. 2^30, bt_stride 1 .. 2^18. */
+typedef struct spin_page_pool {
+    void* data;
+    int64_t page_bytes;
+} spin_page_pool;
+
+/* Re-parents a batch (beam search, parallel sampling, requests leaving): row r of table_out
+ * is row parent[r] of table_in, or empty for parent[r] = -1; ref gains every use in the new
+ * table and loses every use in the old one.  No page is copied: pages a request will write
+ * while they are shared are copied by spin_pages_reserve.
+ * table_out == table_in (in place): rows with parent[r] = r stay, and a row may only continue a
+ * row that stays.  Otherwise the tables must not overlap.  A parent outside [-1, n_req), or in
+ * place one that does not stay, sets BAD_PARENT: the row becomes empty (in place: it stays). */
+spin_status_t spin_pages_fork(int32_t n_req, int64_t n_pages, const int32_t* table_in,
+                              int64_t bt_stride, const int32_t* parent, int32_t* table_out,
+                              int32_t* ref, uint32_t* status, spin_stream_t stream);
+
+/* Releases pages: request r keeps the pages of its first keep_slots[r] slots (0: none) and the
+ * others' entries become -1; keep_slots[r] < 0 leaves the request as it is. */
+spin_status_t spin_pages_free(int32_t n_req, int64_t n_pages, int32_t* block_table,
+                              int64_t bt_stride, const int32_t* keep_slots, int32_t* ref,
+                              uint32_t* status, spin_stream_t stream);
+
+/* Workspace of spin_pages_reserve and spin_pages_compact: 256-byte aligned, uninitialised, not
+ * shared by calls that may run at the same time. */
+spin_status_t spin_pages_workspace_size(int32_t n_req, int64_t n_pages, size_t* bytes);
+
+/* Makes every request's next n_new[r] slots (n_slots[r], n_slots[r]+1, ...) writable: the
+ * blocks they fall in get a fresh page where they have none, or where theirs is shared
+ * (ref > 1, which the request then leaves); a shared page that already holds some of the
+ * request's slots is copied in every pool.  Requests are served in order until the first
+ * whose fresh pages no longer fit: it and all later ones that need any are left as they are
+ * (NO_PAGES).  granted[r] int32 = 1 where the slots are writable, else 0.
+ * Pages that lose their last reference here become free after the call.
+ * n_slots or n_new negative, or blocks past bt_stride: BAD_N, granted 0. */
+spin_status_t spin_pages_reserve(int32_t n_req, int64_t n_pages, int32_t* block_table,
+                                 int64_t bt_stride, const int32_t* n_slots, const int32_t* n_new,
+                                 int32_t* ref, const spin_page_pool* pools, int32_t n_pools,
+                                 int32_t* granted, void* workspace, size_t workspace_bytes,
+                                 uint32_t* status, spin_stream_t stream);
+
+/* Makes the pool dense: with L pages in use, the k-th used page from L on moves into the k-th
+ * free page below L (all pools), and the table entries and reference counts follow it.
+ * *n_live (device int32) = L: afterwards pages 0 .. L-1 are used and the rest are free. */
+spin_status_t spin_pages_compact(int32_t n_req, int64_t n_pages, int32_t* block_table,
+                                 int64_t bt_stride, int32_t* ref, const spin_page_pool* pools,
+                                 int32_t n_pools, int32_t* n_live, void* workspace,
+                                 size_t workspace_bytes, uint32_t* status, spin_stream_t stream);
 
 /* Version string of the library ("spin-gb300 <major>.<minor>.<patch> sm_103a"). */
 const char* spin_version(void);

@@ -513,6 +513,192 @@ spin_status_t spin_selftest_wait(int32_t mode, uint64_t limit_ns, uint32_t* stat
                     "spin_selftest_wait");
 }
 
+static spin_status_t check_kv(const spin_kv_config* c) {
+    g_err[0] = 0;
+    if (!c) return fail(SPIN_ERR_INVALID_ARG, "cfg is NULL");
+    if (c->block != kBlock) return fail(SPIN_ERR_INVALID_ARG, "block must be %d (got %d)", kBlock, c->block);
+    if (c->n_req < 1 || c->n_req > 65535) return fail(SPIN_ERR_INVALID_ARG, "n_req %d outside [1, 65535]", c->n_req);
+    if (c->max_slots < 1 || c->max_slots > (1 << 24))
+        return fail(SPIN_ERR_CAPACITY, "max_slots %d outside [1, 2^24]", c->max_slots);
+    if (c->max_rows < 1 || c->max_rows > kMaxRows)
+        return fail(SPIN_ERR_INVALID_ARG, "max_rows %d outside [1, %d]", c->max_rows, kMaxRows);
+    if (c->n_heads < 1 || c->n_heads > 128) return fail(SPIN_ERR_INVALID_ARG, "n_heads %d outside [1, 128]", c->n_heads);
+    if (c->kv_heads < 1 || c->kv_heads > c->n_heads || c->n_heads % c->kv_heads)
+        return fail(SPIN_ERR_SHAPE, "kv_heads %d must divide n_heads %d", c->kv_heads, c->n_heads);
+    if (c->head_dim < 16 || c->head_dim > 256 || c->head_dim % 16)
+        return fail(SPIN_ERR_INVALID_ARG, "head_dim %d must be a multiple of 16 in [16, 256]", c->head_dim);
+    if (c->dtype != SPIN_DTYPE_F32 && c->dtype != SPIN_DTYPE_BF16 && c->dtype != SPIN_DTYPE_F16)
+        return fail(SPIN_ERR_UNSUPPORTED, "dtype %d: F32, BF16 or F16 only", c->dtype);
+    if (!std::isfinite(c->softmax_scale)) return fail(SPIN_ERR_INVALID_ARG, "softmax_scale is not finite");
+    if (c->reserved != 0) return fail(SPIN_ERR_INVALID_ARG, "reserved must be 0");
+    return SPIN_OK;
+}
+
+static spin_status_t check_kv_rows(const spin_kv_config* c, int32_t rows, int32_t top_k) {
+    if (rows < 1 || rows > c->max_rows)
+        return fail(SPIN_ERR_SHAPE, "rows %d outside [1, max_rows=%d]", rows, c->max_rows);
+    if ((int64_t)c->n_req * rows > 65535) return fail(SPIN_ERR_CAPACITY, "n_req * rows above 65535");
+    if (top_k < 0 || top_k > 16384) return fail(SPIN_ERR_INVALID_ARG, "top_k %d outside [0, 16384]", top_k);
+    return SPIN_OK;
+}
+
+static spin_status_t check_kv_pools(const spin_kv_config* c, const void* k_pool, const void* v_pool,
+                                    const float* k_scale, const float* v_scale, int64_t n_pages,
+                                    const int32_t* block_table, int64_t bt_stride) {
+    if (!k_pool || !v_pool || !k_scale || !v_scale || !block_table)
+        return fail(SPIN_ERR_INVALID_ARG, "k_pool, v_pool, their scales and block_table must be non-NULL");
+    if ((((uintptr_t)k_pool | (uintptr_t)v_pool) & 15) != 0)
+        return fail(SPIN_ERR_INVALID_ARG, "k_pool and v_pool must be 16-byte aligned");
+    if ((((uintptr_t)k_scale | (uintptr_t)v_scale | (uintptr_t)block_table) & 3) != 0)
+        return fail(SPIN_ERR_INVALID_ARG, "the scales and block_table must be 4-byte aligned");
+    if (n_pages < 0 || n_pages > (1ll << 30)) return fail(SPIN_ERR_CAPACITY, "n_pages outside [0, 2^30]");
+    const int64_t mb = ((int64_t)c->max_slots + kBlock - 1) / kBlock;
+    if (bt_stride < mb)
+        return fail(SPIN_ERR_SHAPE, "bt_stride %lld < max blocks %lld", (long long)bt_stride, (long long)mb);
+    return SPIN_OK;
+}
+
+spin_status_t spin_kv_workspace_size(const spin_kv_config* cfg, int32_t rows, int32_t top_k, size_t* bytes) {
+    spin_status_t st = check_kv(cfg);
+    if (st) return st;
+    if ((st = check_kv_rows(cfg, rows, top_k))) return st;
+    if (!bytes) return fail(SPIN_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = kv_attend_workspace_bytes(*cfg, rows, top_k);
+    return SPIN_OK;
+}
+
+spin_status_t spin_kv_attend(const spin_kv_config* cfg, const void* q, const uint8_t* k_pool, const uint8_t* v_pool,
+                             const float* k_scale, const float* v_scale, int64_t n_pages, const int32_t* block_table,
+                             int64_t bt_stride, const int32_t* n_slots, int32_t rows, const int32_t* topk_idx,
+                             int32_t top_k, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                             uint32_t* status, spin_stream_t stream) {
+    spin_status_t st = check_kv(cfg);
+    if (st) return st;
+    if ((st = check_kv_rows(cfg, rows, top_k))) return st;
+    if ((st = check_kv_pools(cfg, k_pool, v_pool, k_scale, v_scale, n_pages, block_table, bt_stride))) return st;
+    if (!q || !n_slots || !out) return fail(SPIN_ERR_INVALID_ARG, "q, n_slots and out must be non-NULL");
+    if ((topk_idx != nullptr) != (top_k > 0))
+        return fail(SPIN_ERR_INVALID_ARG, "topk_idx and top_k > 0 go together");
+    if ((((uintptr_t)q | (uintptr_t)out) & 15) != 0)
+        return fail(SPIN_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+    const size_t need = kv_attend_workspace_bytes(*cfg, rows, top_k);
+    if (!workspace || workspace_bytes < need)
+        return fail(SPIN_ERR_INVALID_ARG, "workspace of %zu bytes needed (got %zu)", need, workspace_bytes);
+    if (((uintptr_t)workspace & 255) != 0) return fail(SPIN_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    KvAttendArgs a{q, k_pool, v_pool, k_scale, v_scale, n_pages, block_table, bt_stride, n_slots, rows, topk_idx,
+                   top_k, out, lse, reinterpret_cast<float*>(workspace), status};
+    return launched(launch_kv_attend(*cfg, a, (cudaStream_t)stream), "spin_kv_attend");
+}
+
+spin_status_t spin_kv_append(const spin_kv_config* cfg, const void* new_k, const void* new_v, int64_t n_tokens,
+                             const int32_t* new_start, int32_t max_new, const int32_t* n_before, uint8_t* k_pool,
+                             uint8_t* v_pool, float* k_scale, float* v_scale, int64_t n_pages,
+                             const int32_t* block_table, int64_t bt_stride, uint32_t* status, spin_stream_t stream) {
+    spin_status_t st = check_kv(cfg);
+    if (st) return st;
+    if ((st = check_kv_pools(cfg, k_pool, v_pool, k_scale, v_scale, n_pages, block_table, bt_stride))) return st;
+    if (!new_start || !n_before || (n_tokens > 0 && (!new_k || !new_v)))
+        return fail(SPIN_ERR_INVALID_ARG, "a required pointer is NULL");
+    if (n_tokens < 0 || n_tokens > INT32_MAX) return fail(SPIN_ERR_CAPACITY, "n_tokens outside [0, 2^31)");
+    if (max_new < 0 || max_new > cfg->max_slots)
+        return fail(SPIN_ERR_INVALID_ARG, "max_new %d outside [0, max_slots=%d]", max_new, cfg->max_slots);
+    if ((((uintptr_t)new_k | (uintptr_t)new_v) & 15) != 0)
+        return fail(SPIN_ERR_INVALID_ARG, "new_k and new_v must be 16-byte aligned");
+    KvAppendArgs a{{new_k, new_v}, {k_pool, v_pool}, {k_scale, v_scale}, n_tokens, new_start, max_new, n_before,
+                   n_pages, block_table, bt_stride, status};
+    return launched(launch_kv_append(*cfg, a, (cudaStream_t)stream), "spin_kv_append");
+}
+
+static spin_status_t check_pages(int32_t n_req, int64_t n_pages, const int32_t* table, int64_t bt_stride,
+                                 const int32_t* ref) {
+    g_err[0] = 0;
+    if (n_req < 1 || n_req > 65535) return fail(SPIN_ERR_INVALID_ARG, "n_req %d outside [1, 65535]", n_req);
+    if (n_pages < 1 || n_pages > (1ll << 30)) return fail(SPIN_ERR_CAPACITY, "n_pages outside [1, 2^30]");
+    if (bt_stride < 1 || bt_stride > (1 << 18)) return fail(SPIN_ERR_CAPACITY, "bt_stride outside [1, 2^18]");
+    if (!table || !ref) return fail(SPIN_ERR_INVALID_ARG, "the block table and ref must be non-NULL");
+    if ((((uintptr_t)table | (uintptr_t)ref) & 3) != 0)
+        return fail(SPIN_ERR_INVALID_ARG, "the block table and ref must be 4-byte aligned");
+    return SPIN_OK;
+}
+
+static spin_status_t check_pools(const spin_page_pool* pools, int32_t n_pools, int32_t n_req, int64_t n_pages,
+                                 const void* workspace, size_t workspace_bytes, PagePoolSet* out) {
+    if (n_pools < 0 || n_pools > kMaxPools)
+        return fail(SPIN_ERR_INVALID_ARG, "n_pools %d outside [0, %d]", n_pools, kMaxPools);
+    if (n_pools > 0 && !pools) return fail(SPIN_ERR_INVALID_ARG, "pools is NULL");
+    out->n = n_pools;
+    for (int32_t i = 0; i < n_pools; ++i) {
+        const spin_page_pool p = pools[i];
+        if (!p.data || ((uintptr_t)p.data & 3) != 0)
+            return fail(SPIN_ERR_INVALID_ARG, "pool %d: data must be non-NULL and 4-byte aligned", i);
+        if (p.page_bytes < 4 || p.page_bytes > (1 << 30) || (p.page_bytes & 3) != 0)
+            return fail(SPIN_ERR_INVALID_ARG, "pool %d: page_bytes must be a multiple of 4 in [4, 2^30]", i);
+        out->pool[i] = p;
+    }
+    const size_t need = pages_workspace_bytes(n_req, n_pages);
+    if (!workspace || workspace_bytes < need)
+        return fail(SPIN_ERR_INVALID_ARG, "workspace of %zu bytes needed (got %zu)", need, workspace_bytes);
+    if (((uintptr_t)workspace & 255) != 0) return fail(SPIN_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    return SPIN_OK;
+}
+
+spin_status_t spin_pages_workspace_size(int32_t n_req, int64_t n_pages, size_t* bytes) {
+    g_err[0] = 0;
+    if (n_req < 1 || n_req > 65535) return fail(SPIN_ERR_INVALID_ARG, "n_req %d outside [1, 65535]", n_req);
+    if (n_pages < 1 || n_pages > (1ll << 30)) return fail(SPIN_ERR_CAPACITY, "n_pages outside [1, 2^30]");
+    if (!bytes) return fail(SPIN_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = pages_workspace_bytes(n_req, n_pages);
+    return SPIN_OK;
+}
+
+spin_status_t spin_pages_fork(int32_t n_req, int64_t n_pages, const int32_t* table_in, int64_t bt_stride,
+                              const int32_t* parent, int32_t* table_out, int32_t* ref, uint32_t* status,
+                              spin_stream_t stream) {
+    spin_status_t st = check_pages(n_req, n_pages, table_out, bt_stride, ref);
+    if (st) return st;
+    if (!table_in || !parent) return fail(SPIN_ERR_INVALID_ARG, "table_in and parent must be non-NULL");
+    const uintptr_t in = (uintptr_t)table_in, out = (uintptr_t)table_out, bytes = (uintptr_t)n_req * bt_stride * 4;
+    if (in != out && in < out + bytes && out < in + bytes)
+        return fail(SPIN_ERR_INVALID_ARG, "table_in and table_out overlap");
+    const PageTable t{n_req, n_pages, table_out, bt_stride, ref, status};
+    return launched(launch_pages_fork(t, table_in, parent, (cudaStream_t)stream), "spin_pages_fork");
+}
+
+spin_status_t spin_pages_free(int32_t n_req, int64_t n_pages, int32_t* block_table, int64_t bt_stride,
+                              const int32_t* keep_slots, int32_t* ref, uint32_t* status, spin_stream_t stream) {
+    spin_status_t st = check_pages(n_req, n_pages, block_table, bt_stride, ref);
+    if (st) return st;
+    if (!keep_slots) return fail(SPIN_ERR_INVALID_ARG, "keep_slots is NULL");
+    const PageTable t{n_req, n_pages, block_table, bt_stride, ref, status};
+    return launched(launch_pages_free(t, keep_slots, (cudaStream_t)stream), "spin_pages_free");
+}
+
+spin_status_t spin_pages_reserve(int32_t n_req, int64_t n_pages, int32_t* block_table, int64_t bt_stride,
+                                 const int32_t* n_slots, const int32_t* n_new, int32_t* ref,
+                                 const spin_page_pool* pools, int32_t n_pools, int32_t* granted, void* workspace,
+                                 size_t workspace_bytes, uint32_t* status, spin_stream_t stream) {
+    spin_status_t st = check_pages(n_req, n_pages, block_table, bt_stride, ref);
+    if (st) return st;
+    if (!n_slots || !n_new || !granted) return fail(SPIN_ERR_INVALID_ARG, "n_slots, n_new and granted must be non-NULL");
+    PagePoolSet set;
+    if ((st = check_pools(pools, n_pools, n_req, n_pages, workspace, workspace_bytes, &set))) return st;
+    const PageTable t{n_req, n_pages, block_table, bt_stride, ref, status};
+    return launched(launch_pages_reserve(t, n_slots, n_new, set, granted, workspace, (cudaStream_t)stream),
+                    "spin_pages_reserve");
+}
+
+spin_status_t spin_pages_compact(int32_t n_req, int64_t n_pages, int32_t* block_table, int64_t bt_stride,
+                                 int32_t* ref, const spin_page_pool* pools, int32_t n_pools, int32_t* n_live,
+                                 void* workspace, size_t workspace_bytes, uint32_t* status, spin_stream_t stream) {
+    spin_status_t st = check_pages(n_req, n_pages, block_table, bt_stride, ref);
+    if (st) return st;
+    if (!n_live) return fail(SPIN_ERR_INVALID_ARG, "n_live is NULL");
+    PagePoolSet set;
+    if ((st = check_pools(pools, n_pools, n_req, n_pages, workspace, workspace_bytes, &set))) return st;
+    const PageTable t{n_req, n_pages, block_table, bt_stride, ref, status};
+    return launched(launch_pages_compact(t, set, n_live, workspace, (cudaStream_t)stream), "spin_pages_compact");
+}
+
 const char* spin_version(void) { return "spin-gb300 0.1.0 sm_103a"; }
 
 const char* spin_last_error_string(void) { return g_err; }

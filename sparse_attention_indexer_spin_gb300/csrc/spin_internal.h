@@ -98,6 +98,68 @@ cudaError_t launch_topk_hint(const spin_config& cfg, const float* scores, const 
 
 int device_sm_count();
 
+// KV cache (spin_kv_append.cu, spin_kv_attend.cu) and its pages (spin_pages.cu).
+struct KvAppendArgs {
+    const void* x[2];       // new keys, new values [n_tokens][kv_heads][head_dim]
+    uint8_t* pool[2];
+    float* scale[2];
+    int64_t n_tokens;
+    const int32_t* new_start;
+    int max_new;
+    const int32_t* n_before;
+    int64_t n_pages;
+    const int32_t* block_table;
+    int64_t bt_stride;
+    uint32_t* status;
+};
+
+struct KvAttendArgs {
+    const void* q;
+    const uint8_t* k_pool;
+    const uint8_t* v_pool;
+    const float* k_scale;
+    const float* v_scale;
+    int64_t n_pages;
+    const int32_t* block_table;
+    int64_t bt_stride;
+    const int32_t* n_slots;
+    int rows;
+    const int32_t* list;    // NULL: every slot
+    int top_k;
+    void* out;
+    float* lse;             // may be NULL
+    float* workspace;
+    uint32_t* status;
+};
+
+constexpr int kMaxPools = 16;
+
+struct PageTable {
+    int32_t n_req;
+    int64_t n_pages;
+    int32_t* table;
+    int64_t stride;
+    int32_t* ref;
+    uint32_t* status;
+};
+
+struct PagePoolSet {
+    spin_page_pool pool[kMaxPools];
+    int n;
+};
+
+cudaError_t launch_kv_append(const spin_kv_config& cfg, const KvAppendArgs& a, cudaStream_t s);
+size_t kv_attend_workspace_bytes(const spin_kv_config& cfg, int rows, int top_k);
+cudaError_t launch_kv_attend(const spin_kv_config& cfg, const KvAttendArgs& a, cudaStream_t s);
+
+size_t pages_workspace_bytes(int32_t n_req, int64_t n_pages);
+cudaError_t launch_pages_fork(const PageTable& t, const int32_t* table_in, const int32_t* parent, cudaStream_t s);
+cudaError_t launch_pages_free(const PageTable& t, const int32_t* keep, cudaStream_t s);
+cudaError_t launch_pages_reserve(const PageTable& t, const int32_t* n_slots, const int32_t* n_new,
+                                 const PagePoolSet& pools, int32_t* granted, void* ws, cudaStream_t s);
+cudaError_t launch_pages_compact(const PageTable& t, const PagePoolSet& pools, int32_t* n_live, void* ws,
+                                 cudaStream_t s);
+
 // Self-test of the bounded mbarrier wait (spin_selftest.cu).
 cudaError_t launch_wait_selftest(int mode, uint64_t limit_ns, uint32_t* status, unsigned long long* elapsed_ns,
                                  cudaStream_t s);

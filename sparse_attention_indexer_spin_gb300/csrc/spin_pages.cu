@@ -1,0 +1,333 @@
+// spin_pages.cu -- page management of paged caches (sm_103a): re-parenting a batch's block
+// tables, releasing pages, making the next slots writable (fresh pages, copies of shared
+// ones) and compacting a pool.
+//
+// The state is a block table and a reference count per page; a page is free while its count
+// is 0.  There is no free list: fresh pages are the lowest free ones, found by a scan over the
+// counts, so a result depends on the state alone and never on the order of atomics (counts
+// are only added to and subtracted from while other threads may).
+#include "spin_common.cuh"
+#include "spin_internal.h"
+
+namespace spin {
+
+constexpr int kPgThreads = 256;
+constexpr int kPlanThreads = 1024;
+constexpr int kCopyBytes = 16 * 1024;  // bytes one CTA copies at a time
+
+// Workspace: a header of 64 words, then prefix [n_req], dst, src and aux [n_pages].
+struct PagesWs {
+    int32_t* count;   // header word 0: entries of dst and src
+    int32_t* live;    // header word 1: pages in use (compaction)
+    int32_t* prefix;  // fresh pages wanted by the requests before this one
+    int32_t* dst;
+    int32_t* src;     // page to copy to dst, -1: none
+    int32_t* aux;     // reserve: page the request leaves, -1: none; compaction: new id of a page
+};
+
+static __host__ __device__ inline int64_t round64(int64_t n) { return (n + 63) & ~(int64_t)63; }
+
+static PagesWs pages_ws(void* ws, int32_t n_req, int64_t n_pages) {
+    int32_t* p = reinterpret_cast<int32_t*>(ws);
+    PagesWs w;
+    w.count = p;
+    w.live = p + 1;
+    w.prefix = p + 64;
+    w.dst = w.prefix + round64(n_req);
+    w.src = w.dst + round64(n_pages);
+    w.aux = w.src + round64(n_pages);
+    return w;
+}
+
+size_t pages_workspace_bytes(int32_t n_req, int64_t n_pages) {
+    return (size_t)(64 + round64(n_req) + 3 * round64(n_pages)) * sizeof(int32_t);
+}
+
+// A table entry as a page, or -1 (BAD_PAGE for anything else outside the pool).
+__device__ __forceinline__ int32_t page_of(int32_t e, const PageTable& t) {
+    if (e >= 0 && e < t.n_pages) return e;
+    if (e != -1) set_status(t.status, SPIN_STATUS_BAD_PAGE);
+    return -1;
+}
+
+// One use less of a page; a count that was already 0 stays there.
+__device__ __forceinline__ void release(int32_t page, const PageTable& t) {
+    if (atomicSub(t.ref + page, 1) <= 0) {
+        atomicAdd(t.ref + page, 1);
+        set_status(t.status, SPIN_STATUS_BAD_REF);
+    }
+}
+
+// ---------------------------------------------------------------------------------- fork
+// One thread per entry of the new table.  In place, a row that changes never serves as a
+// source (checked through `parent`), so the rows read are not written.
+__global__ void __launch_bounds__(kPgThreads)
+pages_fork_kernel(PageTable t, const int32_t* table_in, const int32_t* parent) {
+    pdl_begin();
+    const bool in_place = table_in == t.table;
+    for (int r = blockIdx.y; r < t.n_req; r += gridDim.y) {
+        int p = parent[r];
+        if (in_place && p == r) continue;
+        bool bad = p < -1 || p >= t.n_req;
+        if (in_place && !bad && p >= 0) bad = parent[p] != p;
+        if (bad) {
+            if (threadIdx.x == 0 && blockIdx.x == 0) set_status(t.status, SPIN_STATUS_BAD_PARENT);
+            if (in_place) continue;
+            p = -1;
+        }
+        for (int64_t j = (int64_t)blockIdx.x * kPgThreads + threadIdx.x; j < t.stride; j += (int64_t)gridDim.x * kPgThreads) {
+            const int32_t old = page_of(table_in[r * t.stride + j], t);
+            const int32_t now = p < 0 ? -1 : p == r ? old : page_of(table_in[p * t.stride + j], t);
+            t.table[r * t.stride + j] = now;
+            if (now != old) {
+                if (now >= 0) atomicAdd(t.ref + now, 1);
+                if (old >= 0) release(old, t);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------- free
+__global__ void __launch_bounds__(kPgThreads) pages_free_kernel(PageTable t, const int32_t* keep) {
+    pdl_begin();
+    for (int r = blockIdx.y; r < t.n_req; r += gridDim.y) {
+        const int k = keep[r];
+        if (k < 0) continue;
+        const int64_t first = (k >> 6) + ((k & 63) != 0);
+        for (int64_t j = first + (int64_t)blockIdx.x * kPgThreads + threadIdx.x; j < t.stride;
+             j += (int64_t)gridDim.x * kPgThreads) {
+            const int32_t e = t.table[r * t.stride + j];
+            if (e == -1) continue;
+            const int32_t old = page_of(e, t);
+            t.table[r * t.stride + j] = -1;
+            if (old >= 0) release(old, t);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------- reserve
+struct Span {
+    int64_t j0, j1;   // blocks [j0, j1) the next slots fall in
+    bool partial;     // the first of them already holds some of the request's slots
+    bool bad;
+};
+
+__device__ __forceinline__ Span span_of(int32_t n, int32_t add, int64_t stride) {
+    Span s{0, 0, false, n < 0 || add < 0};
+    if (s.bad || add == 0) return s;
+    s.j0 = n >> 6;
+    s.j1 = ((int64_t)n + add + 63) >> 6;
+    s.partial = (n & 63) != 0;
+    s.bad = s.j1 > stride;
+    if (s.bad) s.j1 = s.j0;
+    return s;
+}
+
+// Whether block j needs a fresh page; *old is the page it has (-1: none).
+__device__ __forceinline__ bool needs_page(const PageTable& t, int64_t at, int32_t* old) {
+    const int32_t e = t.table[at];
+    *old = e >= 0 && e < t.n_pages ? e : -1;
+    return *old < 0 || t.ref[*old] > 1;
+}
+
+// The plan, by one CTA: (1) count each request's fresh pages and their prefix, (2) list the
+// lowest free pages, (3) hand them out, (4) move the reference counts.  Every decision in (3)
+// reads the counts as they were at the start; only (4) changes them.
+__global__ void __launch_bounds__(kPlanThreads)
+pages_reserve_kernel(PageTable t, const int32_t* n_slots, const int32_t* n_new, int32_t* granted, PagesWs w) {
+    pdl_begin();
+    __shared__ int s_scan[33];
+    __shared__ int s_given;
+    const int tid = threadIdx.x;
+    constexpr int kMost = 1 << 30;  // prefix sums saturate here (n_pages <= 2^30)
+    int carry = 0, sum;
+    if (tid == 0) s_given = 0;
+    for (int base = 0; base < t.n_req; base += kPlanThreads) {
+        const int r = base + tid;
+        int need = 0;
+        if (r < t.n_req) {
+            const Span sp = span_of(n_slots[r], n_new[r], t.stride);
+            if (sp.bad) set_status(t.status, SPIN_STATUS_BAD_N);
+            int32_t old;
+            for (int64_t j = sp.j0; j < sp.j1; ++j) {
+                page_of(t.table[r * t.stride + j], t);
+                need += needs_page(t, r * t.stride + j, &old);
+            }
+        }
+        const int pre = block_excl_scan(need, s_scan, &sum);
+        if (r < t.n_req) w.prefix[r] = min(kMost, carry + pre);
+        carry = min(kMost, carry + sum);
+    }
+    const int total = carry;
+    int found = 0;
+    for (int64_t base = 0; base < t.n_pages && found < total; base += kPlanThreads) {
+        const int64_t p = base + tid;
+        const int is_free = p < t.n_pages && t.ref[p] <= 0;
+        const int rank = found + block_excl_scan(is_free, s_scan, &sum);
+        if (is_free && rank < total) w.dst[rank] = (int32_t)p;
+        found += sum;
+    }
+    found = min(found, total);
+    __syncthreads();
+    for (int r = tid; r < t.n_req; r += kPlanThreads) {
+        const Span sp = span_of(n_slots[r], n_new[r], t.stride);
+        int need = 0;
+        int32_t old;
+        for (int64_t j = sp.j0; j < sp.j1; ++j) need += needs_page(t, r * t.stride + j, &old);
+        const int64_t first = w.prefix[r];
+        const bool ok = need == 0 || first + need <= found;
+        granted[r] = ok && !sp.bad;
+        if (!ok) set_status(t.status, SPIN_STATUS_NO_PAGES);
+        if (!ok || need == 0) continue;
+        int64_t k = first;
+        for (int64_t j = sp.j0; j < sp.j1; ++j) {
+            if (!needs_page(t, r * t.stride + j, &old)) continue;
+            t.table[r * t.stride + j] = w.dst[k];
+            w.aux[k] = old;
+            w.src[k] = old >= 0 && sp.partial && j == sp.j0 ? old : -1;
+            ++k;
+        }
+        atomicMax(&s_given, (int)k);
+    }
+    __syncthreads();
+    const int given = s_given;
+    for (int k = tid; k < given; k += kPlanThreads) {
+        t.ref[w.dst[k]] = 1;
+        if (w.aux[k] >= 0) release(w.aux[k], t);
+    }
+    if (tid == 0) *w.count = given;
+}
+
+// ------------------------------------------------------------------------------- compact
+// The plan, by one CTA: the number L of pages in use, the used pages from L on (src) and the
+// free ones below L (dst), both ascending, and the new id of every page from L on (aux).
+__global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(PageTable t, int32_t* n_live, PagesWs w) {
+    pdl_begin();
+    __shared__ int s_scan[33];
+    const int tid = threadIdx.x;
+    int cnt = 0, live;
+    for (int64_t p = tid; p < t.n_pages; p += kPlanThreads) cnt += t.ref[p] > 0;
+    block_excl_scan(cnt, s_scan, &live);
+    int holes = 0, moves = 0, sum;
+    for (int64_t base = 0; base < t.n_pages; base += kPlanThreads) {
+        const int64_t p = base + tid;
+        const bool used = p < t.n_pages && t.ref[p] > 0;
+        const int hole = p < live && !used, move = p >= live && used;
+        const int rh = block_excl_scan(hole, s_scan, &sum);
+        if (hole) w.dst[holes + rh] = (int32_t)p;
+        holes += sum;
+        const int rm = block_excl_scan(move, s_scan, &sum);
+        if (move) w.src[moves + rm] = (int32_t)p;
+        moves += sum;
+    }
+    __syncthreads();
+    for (int64_t p = live + tid; p < t.n_pages; p += kPlanThreads) w.aux[p] = -1;
+    __syncthreads();
+    for (int k = tid; k < moves; k += kPlanThreads) w.aux[w.src[k]] = w.dst[k];
+    if (tid == 0) {
+        *w.count = moves;
+        *w.live = live;
+        *n_live = live;
+    }
+}
+
+__global__ void __launch_bounds__(kPgThreads) pages_remap_kernel(PageTable t, PagesWs w) {
+    pdl_begin();
+    const int64_t me = (int64_t)blockIdx.x * kPgThreads + threadIdx.x, all = (int64_t)gridDim.x * kPgThreads;
+    const int live = *w.live, moves = *w.count;
+    for (int64_t i = me; i < (int64_t)t.n_req * t.stride; i += all) {
+        const int32_t e = page_of(t.table[i], t);
+        if (e < live) continue;
+        const int32_t to = w.aux[e];
+        if (to >= 0) t.table[i] = to;
+        else set_status(t.status, SPIN_STATUS_BAD_REF);
+    }
+    for (int64_t k = me; k < moves; k += all) {
+        t.ref[w.dst[k]] = t.ref[w.src[k]];
+        t.ref[w.src[k]] = 0;
+    }
+}
+
+// ------------------------------------------------------------------------------- copying
+// Pages src[k] -> dst[k] of every pool, in chunks of kCopyBytes.  No source is a destination.
+__global__ void __launch_bounds__(kPgThreads) pages_copy_kernel(PagePoolSet pools, PagesWs w, int chunks) {
+    pdl_begin();
+    const int64_t items = (int64_t)*w.count * chunks;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const int k = (int)(it / chunks);
+        int c = (int)(it % chunks);
+        const int32_t src = w.src[k], dst = w.dst[k];
+        if (src < 0) continue;
+        int p = 0;
+        for (;; ++p) {
+            const int n = (int)((pools.pool[p].page_bytes + kCopyBytes - 1) / kCopyBytes);
+            if (c < n) break;
+            c -= n;
+        }
+        const int64_t bytes = pools.pool[p].page_bytes, off = (int64_t)c * kCopyBytes;
+        const int n = (int)(bytes - off < kCopyBytes ? bytes - off : kCopyBytes);
+        const char* from = (const char*)pools.pool[p].data + src * bytes + off;
+        char* to = (char*)pools.pool[p].data + dst * bytes + off;
+        if ((((uintptr_t)pools.pool[p].data | (uintptr_t)bytes) & 15) == 0) {
+            uint4 v[kCopyBytes / 16 / kPgThreads];
+#pragma unroll
+            for (int i = 0; i < kCopyBytes / 16 / kPgThreads; ++i) {
+                const int e = (int)threadIdx.x + i * kPgThreads;
+                if (e * 16 < n) v[i] = reinterpret_cast<const uint4*>(from)[e];
+            }
+#pragma unroll
+            for (int i = 0; i < kCopyBytes / 16 / kPgThreads; ++i) {
+                const int e = (int)threadIdx.x + i * kPgThreads;
+                if (e * 16 < n) reinterpret_cast<uint4*>(to)[e] = v[i];
+            }
+        } else {
+            for (int e = threadIdx.x; e * 4 < n; e += kPgThreads)
+                reinterpret_cast<uint32_t*>(to)[e] = reinterpret_cast<const uint32_t*>(from)[e];
+        }
+    }
+}
+
+static int copy_chunks(const PagePoolSet& pools) {
+    int64_t n = 0;
+    for (int i = 0; i < pools.n; ++i) n += (pools.pool[i].page_bytes + kCopyBytes - 1) / kCopyBytes;
+    return (int)n;
+}
+
+static dim3 table_grid(const PageTable& t) {
+    const int64_t x = (t.stride + kPgThreads - 1) / kPgThreads;
+    return dim3((unsigned)(x < 64 ? x : 64), (unsigned)t.n_req);
+}
+
+cudaError_t launch_pages_fork(const PageTable& t, const int32_t* table_in, const int32_t* parent, cudaStream_t s) {
+    return launch_pdl(pages_fork_kernel, table_grid(t), dim3(kPgThreads), 0, s, nullptr, 0, t, table_in, parent);
+}
+
+cudaError_t launch_pages_free(const PageTable& t, const int32_t* keep, cudaStream_t s) {
+    return launch_pdl(pages_free_kernel, table_grid(t), dim3(kPgThreads), 0, s, nullptr, 0, t, keep);
+}
+
+static cudaError_t launch_copy(const PagePoolSet& pools, const PagesWs& w, cudaStream_t s) {
+    const int chunks = copy_chunks(pools);
+    if (chunks == 0) return cudaSuccess;
+    return launch_pdl(pages_copy_kernel, dim3(8 * device_sm_count()), dim3(kPgThreads), 0, s, nullptr, 0, pools, w,
+                      chunks);
+}
+
+cudaError_t launch_pages_reserve(const PageTable& t, const int32_t* n_slots, const int32_t* n_new,
+                                 const PagePoolSet& pools, int32_t* granted, void* ws, cudaStream_t s) {
+    const PagesWs w = pages_ws(ws, t.n_req, t.n_pages);
+    cudaError_t e = launch_pdl(pages_reserve_kernel, dim3(1), dim3(kPlanThreads), 0, s, nullptr, 0, t, n_slots, n_new,
+                               granted, w);
+    return e != cudaSuccess ? e : launch_copy(pools, w, s);
+}
+
+cudaError_t launch_pages_compact(const PageTable& t, const PagePoolSet& pools, int32_t* n_live, void* ws,
+                                 cudaStream_t s) {
+    const PagesWs w = pages_ws(ws, t.n_req, t.n_pages);
+    cudaError_t e = launch_pdl(pages_compact_kernel, dim3(1), dim3(kPlanThreads), 0, s, nullptr, 0, t, n_live, w);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(pages_remap_kernel, dim3(device_sm_count()), dim3(kPgThreads), 0, s, nullptr, 0, t, w);
+    return e != cudaSuccess ? e : launch_copy(pools, w, s);
+}
+
+}  // namespace spin

@@ -18,7 +18,8 @@ ROOT = os.path.dirname(PKG)
 LIB_PATH = os.path.join(PKG, "libspin.so")
 HEADER = os.path.join(ROOT, "include", "spin.h")
 
-DTYPE = {"f32": 0, "bf16": 1, "e4m3": 2}
+DTYPE = {"f32": 0, "bf16": 1, "e4m3": 2, "f16": 3}
+TORCH_DTYPE = {0: torch.float32, 1: torch.bfloat16, 3: torch.float16}
 COMBINE = {"max": 0, "sum": 1}
 POOLING = {"max": 0, "mean": 1, "top4": 2, "slots": 3, "a2": 4}
 EXPLORE = {"random": 0, "age": 1}
@@ -26,7 +27,8 @@ SCORE_PATH = {"auto": 0, "generic": 1, "stream": 2, "tcgen05": 3}
 
 STATUS_BITS = {
     "BAD_N": 0x01, "BAD_QPOS": 0x02, "BAD_LIST": 0x04, "BAD_PAGE": 0x08,
-    "BAD_ACCEPTED": 0x10, "TIMEOUT": 0x20, "BAD_RHO": 0x40,
+    "BAD_ACCEPTED": 0x10, "TIMEOUT": 0x20, "BAD_RHO": 0x40, "BAD_PARENT": 0x80, "BAD_REF": 0x100,
+    "NO_PAGES": 0x200,
 }
 
 ERRORS = {0: "SPIN_OK", 1: "SPIN_ERR_INVALID_ARG", 2: "SPIN_ERR_SHAPE", 3: "SPIN_ERR_CAPACITY",
@@ -63,6 +65,19 @@ class SpinConfig(ctypes.Structure):
         return self.max_slots + self.max_rows
 
 
+class SpinKvConfig(ctypes.Structure):
+    _fields_ = [
+        ("n_req", ctypes.c_int32), ("max_slots", ctypes.c_int32), ("max_rows", ctypes.c_int32),
+        ("block", ctypes.c_int32), ("n_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class SpinPagePool(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("page_bytes", ctypes.c_int64)]
+
+
 def make_config(n_req, max_slots, max_rows, n_heads, head_dim, kv_heads, q_dtype, k_dtype, top_k,
                 rho_bp, gamma_bp, alpha, combine="max", seed=0, block=64, score_path="auto",
                 pooling="max", explore="random", **_ignored) -> SpinConfig:
@@ -71,6 +86,15 @@ def make_config(n_req, max_slots, max_rows, n_heads, head_dim, kv_heads, q_dtype
                       int(rho_bp), int(gamma_bp), float(alpha), COMBINE[combine],
                       int(seed) & 0xFFFFFFFFFFFFFFFF, SCORE_PATH[score_path], POOLING[pooling],
                       EXPLORE[explore], 0)
+
+
+def make_kv_config(n_req, max_slots, max_rows, n_heads, kv_heads, head_dim, dtype, softmax_scale=None,
+                   block=64) -> SpinKvConfig:
+    """softmax_scale: 1 / sqrt(head_dim) by default."""
+    if softmax_scale is None:
+        softmax_scale = head_dim ** -0.5
+    return SpinKvConfig(int(n_req), int(max_slots), int(max_rows), int(block), int(n_heads), int(kv_heads),
+                        int(head_dim), DTYPE[dtype], float(softmax_scale), 0)
 
 
 def ensure_built() -> str:
@@ -90,6 +114,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         P, i32, i64, u64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64
         C = ctypes.POINTER(SpinConfig)
+        K = ctypes.POINTER(SpinKvConfig)
         sig = {
             "spin_init_state": [C, P, P, P, P, i32, P],
             "spin_select_blocks": [C, P, P, P, P, P, P, i32, P, u64, i32, P, P, P, P, P,
@@ -114,6 +139,14 @@ def lib():
             "spin_update_ema_age": [C, P, P, P, P, P, P, P, P, P, P, u64, P, P],
             "spin_commit_mtp": [C, P, P, P, P, P, i32, P, P, P, P, P, P, P],
             "spin_workspace_size": [C, i32, ctypes.POINTER(ctypes.c_size_t)],
+            "spin_kv_workspace_size": [K, i32, i32, ctypes.POINTER(ctypes.c_size_t)],
+            "spin_kv_attend": [K, P, P, P, P, P, i64, P, i64, P, i32, P, i32, P, P, P, ctypes.c_size_t, P, P],
+            "spin_kv_append": [K, P, P, i64, P, i32, P, P, P, P, P, i64, P, i64, P, P],
+            "spin_pages_workspace_size": [i32, i64, ctypes.POINTER(ctypes.c_size_t)],
+            "spin_pages_fork": [i32, i64, P, i64, P, P, P, P, P],
+            "spin_pages_free": [i32, i64, P, i64, P, P, P, P],
+            "spin_pages_reserve": [i32, i64, P, i64, P, P, P, P, i32, P, P, ctypes.c_size_t, P, P],
+            "spin_pages_compact": [i32, i64, P, i64, P, P, i32, P, P, ctypes.c_size_t, P, P],
             "spin_selftest_wait": [i32, u64, P, P, P],
             "spin_miss_curve": [P, i32, i64, P, P, i32, i32, P],
             "spin_allocate_budgets": [P, i32, i32, i32, i32, P, P],
@@ -367,6 +400,172 @@ def commit_mtp(cfg, V, D, Vmax, warm, scores, rows, union_blocks, n_union, n_slo
                                  _ptr(scores), rows, _ptr(union_blocks), _ptr(n_union),
                                  _ptr(n_slots), _ptr(q_pos), _ptr(accepted), _ptr(status),
                                  _stream(stream)))
+
+
+# --------------------------------------------------------------------------- KV cache
+# The calls below check their tensors' types, shapes and device before they pass them on: every
+# tensor must be contiguous and on the current device (a wrong shape would be read past its end).
+
+def _arg(name, t, dtype, shape, device):
+    """The address of a tensor argument of exactly this type and shape on `device`."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise SpinError(1, "%s must be a contiguous %s tensor of shape %s on the current device (cuda:%d); got %s %s "
+                        "on %s%s" % (name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device,
+                                     "" if t.is_contiguous() else ", not contiguous"))
+    return t.data_ptr()
+
+
+def _kv_pool_args(cfg, k, v, k_scale, v_scale, block_table, dev):
+    n = k.shape[0]
+    pool, scale = (n, 64, cfg.kv_heads, cfg.head_dim), (n, cfg.kv_heads)
+    bt = block_table.shape[-1]
+    return (_arg("k", k, torch.uint8, pool, dev), _arg("v", v, torch.uint8, pool, dev),
+            _arg("k_scale", k_scale, torch.float32, scale, dev), _arg("v_scale", v_scale, torch.float32, scale, dev),
+            n, _arg("block_table", block_table, torch.int32, (cfg.n_req, bt), dev), bt)
+
+
+def _status_arg(status, dev):
+    return None if status is None else _arg("status", status, torch.int32, (1,), dev)
+
+
+def _workspace_arg(workspace, dev):
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise SpinError(1, "workspace must be a contiguous tensor on the current device (cuda:%d)" % dev)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def kv_workspace(cfg: SpinKvConfig, rows: int = 1, top_k: int = 0, device="cuda"):
+    """A workspace for kv_attend (spin_kv_workspace_size bytes)."""
+    out = ctypes.c_size_t(0)
+    _check(lib().spin_kv_workspace_size(ctypes.byref(cfg), rows, top_k, ctypes.byref(out)))
+    return torch.empty(int(out.value), dtype=torch.uint8, device=device)
+
+
+def kv_attend(cfg, q, k, v, k_scale, v_scale, block_table, n_slots, rows, topk_idx, out, lse, workspace, status,
+              stream=None):
+    """spin_kv_attend: attention of q [R][rows][n_heads][d] over the cache, over every slot
+    (topk_idx None) or over the listed ones [R][rows][K].  n_slots int32 [R][rows]; lse fp32
+    [R][rows][n_heads] or None."""
+    dev = torch.cuda.current_device()
+    R, t, shape = cfg.n_req, TORCH_DTYPE.get(cfg.dtype), (cfg.n_req, rows, cfg.n_heads, cfg.head_dim)
+    top_k = 0 if topk_idx is None else topk_idx.shape[-1]
+    ws, ws_bytes = _workspace_arg(workspace, dev)
+    _check(lib().spin_kv_attend(
+        ctypes.byref(cfg), _arg("q", q, t, shape, dev),
+        *_kv_pool_args(cfg, k, v, k_scale, v_scale, block_table, dev),
+        _arg("n_slots", n_slots, torch.int32, (R, rows), dev), rows,
+        None if topk_idx is None else _arg("topk_idx", topk_idx, torch.int32, (R, rows, top_k), dev), top_k,
+        _arg("out", out, t, shape, dev),
+        None if lse is None else _arg("lse", lse, torch.float32, shape[:3], dev), ws, ws_bytes,
+        _status_arg(status, dev), _stream(stream)))
+
+
+def kv_append(cfg, new_k, new_v, new_start, max_new, n_before, k, v, k_scale, v_scale, block_table, status,
+              stream=None):
+    """spin_kv_append: new_k, new_v [T][kv_heads][d]; request r's tokens new_start[r] ..
+    new_start[r+1]-1 (at most max_new) go to its slots from n_before[r] on."""
+    dev = torch.cuda.current_device()
+    T, t = new_k.shape[0], TORCH_DTYPE.get(cfg.dtype)
+    shape = (T, cfg.kv_heads, cfg.head_dim)
+    _check(lib().spin_kv_append(
+        ctypes.byref(cfg), _arg("new_k", new_k, t, shape, dev), _arg("new_v", new_v, t, shape, dev), T,
+        _arg("new_start", new_start, torch.int32, (cfg.n_req + 1,), dev), max_new,
+        _arg("n_before", n_before, torch.int32, (cfg.n_req,), dev),
+        *_kv_pool_args(cfg, k, v, k_scale, v_scale, block_table, dev), _status_arg(status, dev), _stream(stream)))
+
+
+class KvCache:
+    """Device buffers of one layer's 8-bit KV cache (allocated by PyTorch): codes and scales."""
+
+    def __init__(self, n_pages: int, kv_heads: int, head_dim: int, device="cuda"):
+        shape = (n_pages, 64, kv_heads, head_dim)
+        self.k = torch.zeros(shape, dtype=torch.uint8, device=device)
+        self.v = torch.zeros(shape, dtype=torch.uint8, device=device)
+        self.k_scale = torch.zeros((n_pages, kv_heads), dtype=torch.float32, device=device)
+        self.v_scale = torch.zeros((n_pages, kv_heads), dtype=torch.float32, device=device)
+
+    @property
+    def tensors(self):
+        return self.k, self.v, self.k_scale, self.v_scale
+
+
+class PagePools:
+    """The arrays indexed by page that move with it: contiguous tensors [n_pages, ...] on one
+    device.  Keeps them alive; a layer stack lists every layer's."""
+
+    def __init__(self, *tensors):
+        self.tensors = tensors
+        self.n_pages = tensors[0].shape[0]
+        self.device = tensors[0].get_device()
+        for i, t in enumerate(tensors):
+            if t.shape[0] != self.n_pages or t.get_device() != self.device or not t.is_contiguous() or not t.is_cuda:
+                raise SpinError(1, "pool %d: contiguous CUDA tensors of as many pages on one device" % i)
+        self.array = (SpinPagePool * len(tensors))(
+            *[SpinPagePool(t.data_ptr(), t.numel() // self.n_pages * t.element_size()) for t in tensors])
+
+
+def pages_workspace(n_req: int, n_pages: int, device="cuda"):
+    """A workspace for pages_reserve and pages_compact (spin_pages_workspace_size bytes)."""
+    out = ctypes.c_size_t(0)
+    _check(lib().spin_pages_workspace_size(n_req, n_pages, ctypes.byref(out)))
+    return torch.empty(int(out.value), dtype=torch.uint8, device=device)
+
+
+def _table_args(name, table, dev):
+    return _arg(name, table, torch.int32, tuple(table.shape[-2:]), dev)
+
+
+def _ref_arg(ref, dev):
+    return _arg("ref", ref, torch.int32, (ref.numel(),), dev)
+
+
+def _pools_of(pools, n_pages, dev):
+    if pools.n_pages != n_pages or pools.device != dev:
+        raise SpinError(1, "the pools must have ref's %d pages and be on the current device" % n_pages)
+    return pools.array, len(pools.array)
+
+
+def pages_fork(table_in, parent, table_out, ref, status, stream=None):
+    """spin_pages_fork: row r of table_out becomes row parent[r] of table_in (-1: empty)."""
+    dev = torch.cuda.current_device()
+    R, bt = table_out.shape
+    _check(lib().spin_pages_fork(
+        R, ref.numel(), _arg("table_in", table_in, torch.int32, (R, bt), dev), bt,
+        _arg("parent", parent, torch.int32, (R,), dev), _table_args("table_out", table_out, dev), _ref_arg(ref, dev),
+        _status_arg(status, dev), _stream(stream)))
+
+
+def pages_free(block_table, keep_slots, ref, status, stream=None):
+    """spin_pages_free: request r keeps the pages of its first keep_slots[r] slots (< 0: all)."""
+    dev = torch.cuda.current_device()
+    R, bt = block_table.shape
+    _check(lib().spin_pages_free(
+        R, ref.numel(), _table_args("block_table", block_table, dev), bt,
+        _arg("keep_slots", keep_slots, torch.int32, (R,), dev), _ref_arg(ref, dev), _status_arg(status, dev),
+        _stream(stream)))
+
+
+def pages_reserve(block_table, n_slots, n_new, ref, pools, granted, workspace, status, stream=None):
+    """spin_pages_reserve: makes the next n_new[r] slots of every request writable."""
+    dev = torch.cuda.current_device()
+    R, bt = block_table.shape
+    ws, ws_bytes = _workspace_arg(workspace, dev)
+    _check(lib().spin_pages_reserve(
+        R, ref.numel(), _table_args("block_table", block_table, dev), bt,
+        _arg("n_slots", n_slots, torch.int32, (R,), dev), _arg("n_new", n_new, torch.int32, (R,), dev),
+        _ref_arg(ref, dev), *_pools_of(pools, ref.numel(), dev), _arg("granted", granted, torch.int32, (R,), dev),
+        ws, ws_bytes, _status_arg(status, dev), _stream(stream)))
+
+
+def pages_compact(block_table, ref, pools, n_live, workspace, status, stream=None):
+    """spin_pages_compact: moves the used pages to the lowest ids; n_live int32 [1]."""
+    dev = torch.cuda.current_device()
+    R, bt = block_table.shape
+    ws, ws_bytes = _workspace_arg(workspace, dev)
+    _check(lib().spin_pages_compact(
+        R, ref.numel(), _table_args("block_table", block_table, dev), bt, _ref_arg(ref, dev),
+        *_pools_of(pools, ref.numel(), dev), _arg("n_live", n_live, torch.int32, (1,), dev), ws, ws_bytes,
+        _status_arg(status, dev), _stream(stream)))
 
 
 # ------------------------------------------------------------------------ convenience

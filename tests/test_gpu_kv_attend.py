@@ -1,0 +1,271 @@
+"""Attention over the paged 8-bit KV cache against its definition in 64 bits.
+
+Tolerances.  With w the softmax weights, A = sum w |v| and S = max softmax_scale ks sum |q||k|:
+  * a score is a fp32 dot product of d exact products, accumulated 16 at a time (each step off
+    by at most 2^-22 of the magnitude bound), then scaled and turned into an exponent with a few
+    fp32 roundings: |ds| <= es = (d/16 + 4) 2^-22 S + 2^-22 (|s| + 8), where the 8 also covers
+    the exponential's relative error;
+  * it moves a weight and the weights' sum by e^es each: 2 es A;
+  * a weight enters its product rounded to f16 (bf16 and f16: 2^-11) or to two f16 terms (f32:
+    2^-22, doubled here): ew A, with weights far below the largest (2^-14 after its scaling by at
+    least 2^10) off by at most 2^-37 of the largest weight times value scale times 448;
+  * the weights' sum and the product's sum are accumulated in fp32: el = (n/16 + 8) 2^-22 each;
+  * the result is rounded once: half a step of the output's type.
+lse = ln of the sum: es + el, and fp32 roundings of its own, relative 2^-22.
+"""
+import numpy as np
+import pytest
+import torch
+
+import _kv
+from oracle import kv as o
+from sparse_attention_indexer_spin_gb300 import spin
+
+pytestmark = pytest.mark.gpu
+
+
+def check(dtype, heads, kvh, d, lens, rows=1, top_k=0, seed=0, spread=0.3, scale=None, n_slots=None, listed=None,
+          mutate=None, status_bits=0, q_size=1.0):
+    """One call against the oracle; `lens` are the requests' cached slots."""
+    rng = np.random.default_rng(seed)
+    R = len(lens)
+    n_pages = sum(-(-int(n) // 64) for n in lens) + 3
+    pools = list(_kv.make_pools(rng, n_pages, kvh, d, spread))
+    table = _kv.make_table(rng, lens, n_pages)
+    if n_slots is None:                # row r of a verification sees one slot more than row r - 1
+        n_slots = np.maximum(np.asarray(lens)[:, None] - np.arange(rows - 1, -1, -1), 0)
+    n_slots = np.ascontiguousarray(n_slots, dtype=np.int32)
+    q = torch.from_numpy(rng.normal(size=(R, rows, heads, d)) * q_size).to(_kv.TYPES[dtype])
+    if top_k and listed is None:
+        listed = np.full((R, rows, top_k), -1, np.int32)
+        for b in range(R):
+            for r in range(rows):
+                m = min(top_k, int(n_slots[b, r]))
+                listed[b, r, :m] = np.sort(rng.permutation(int(n_slots[b, r]))[:m])
+    if mutate:
+        mutate(rng, pools, table, n_slots, listed)
+    cfg = spin.make_kv_config(R, max(max(lens), 1), rows, heads, kvh, d, dtype, scale)
+    dv = [_kv.dev(x) for x in pools]
+    before = [x.clone() for x in dv]
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dl = None if listed is None else _kv.dev(listed)
+    out, lse = _kv.run_attend(cfg, q.cuda(), dv, _kv.dev(table), _kv.dev(n_slots), rows, dl, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == status_bits
+    for x, y in zip(dv, before):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))   # the cache is only read
+    good = np.where((n_slots < 0) | (n_slots > cfg.max_slots), 0, n_slots)
+    ref, rlse, info = o.attend(q.double().numpy(), *pools, table, good, cfg.softmax_scale, listed)
+    tol, ltol = _kv.attend_tolerance(dtype, d, ref, info)
+    got, glse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    nan = np.isnan(ref)
+    assert np.array_equal(np.isnan(got), nan)
+    err = np.abs(got - ref)
+    assert (err[~nan] <= tol[~nan]).all(), float((err[~nan] / tol[~nan]).max())
+    empty = np.isneginf(rlse)
+    assert np.array_equal(np.isneginf(glse), empty)
+    assert (got[empty] == 0).all()
+    ok = ~empty & ~np.isnan(rlse)
+    assert (np.abs(glse[ok] - rlse[ok]) <= ltol[ok] + 2.0 ** -22 * (np.abs(rlse[ok]) + 1)).all()
+    # without lse the output is the same
+    out2, _ = _kv.run_attend(cfg, q.cuda(), dv, _kv.dev(table), _kv.dev(n_slots), rows, dl, want_lse=False)
+    assert torch.equal(out.view(torch.uint8), out2.view(torch.uint8))
+    return out, lse
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("heads,kvh", [(8, 8), (32, 8), (5, 5), (28, 4), (64, 1), (128, 1), (1, 1)])
+def test_head_layouts(dtype, heads, kvh):
+    check(dtype, heads, kvh, 128, [1, 200, 0, 64, 321], seed=heads)
+
+
+@pytest.mark.parametrize("d", [16, 32, 48, 64, 80, 96, 112, 128, 144, 192, 240, 256])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_head_dims(dtype, d):
+    check(dtype, 6, 2, d, [130, 65, 7], seed=d)
+    check(dtype, 6, 2, d, [130, 65, 7], seed=d, rows=2, top_k=33)
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 511, 1000, 5000])
+def test_lengths(n):
+    check("bf16", 16, 2, 128, [n], seed=n)
+    check("f32", 8, 8, 64, [n, 1], seed=n)
+
+
+@pytest.mark.parametrize("rows", [1, 2, 3, 4, 8])
+@pytest.mark.parametrize("heads,kvh", [(8, 8), (16, 2), (64, 1), (128, 2)])
+def test_rows(rows, heads, kvh):
+    """Verifier rows that see one slot more each, across a page's end and from no slots on."""
+    check("bf16", heads, kvh, 128, [rows + 63, 66, 2, 0, 700], rows=rows, seed=rows)
+    check("f16", heads, kvh, 64, [rows + 63, 66, 2, 0, 700], rows=rows, seed=rows)
+
+
+@pytest.mark.parametrize("top_k", [1, 7, 64, 100, 256, 512, 2048])
+@pytest.mark.parametrize("heads,kvh,rows", [(64, 1, 1), (8, 8, 3), (32, 8, 1), (12, 1, 2)])
+def test_lists(top_k, heads, kvh, rows):
+    check("bf16", heads, kvh, 128, [3000, 50, 0, 1, 777], rows=rows, top_k=top_k, seed=top_k)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_many_requests_of_mixed_length(dtype):
+    rng = np.random.default_rng(5)
+    lens = np.exp(rng.uniform(0, np.log(3000), 70)).astype(int)
+    lens[::9] = 0
+    check(dtype, 8, 2, 64, list(lens), seed=6)
+
+
+def test_long_context():
+    check("bf16", 16, 2, 128, [40000, 3], seed=1)
+    check("f32", 2, 1, 64, [40000], seed=1)
+
+
+@pytest.mark.parametrize("scale", [0.0, 1.0, -0.5, 3.0])
+def test_softmax_scale(scale):
+    """Flat, sharp and inverted weights."""
+    check("bf16", 8, 2, 128, [300, 40], scale=scale, seed=3)
+    check("f32", 8, 2, 64, [300, 40], scale=scale, seed=3)
+
+
+@pytest.mark.parametrize("spread", [0.0, 3.0, 6.0])
+def test_scales_of_very_different_pages(spread):
+    """Value scales e^+-18 apart: the small pages' products must not be lost beside the large
+    ones' scale."""
+    check("bf16", 8, 2, 128, [700, 64], spread=spread, seed=4, scale=1e-3)
+    check("f32", 8, 2, 128, [700, 64], spread=spread, seed=4, scale=1e-3)
+
+
+@pytest.mark.parametrize("dtype,size", [("bf16", 1e-30), ("bf16", 1e25), ("f32", 1e-25), ("f32", 1e20), ("f16", 1e-4)])
+def test_queries_of_extreme_size(dtype, size):
+    check(dtype, 8, 2, 64, [100, 30], q_size=size, scale=0.1 / size if dtype != "f16" else 30.0, seed=8)
+
+
+def _zero_pages(rng, pools, table, n_slots, listed):
+    for x in pools[2:]:
+        x[rng.permutation(len(x))[: len(x) // 2]] = 0.0
+
+
+def test_pages_of_scale_zero():
+    check("bf16", 8, 2, 128, [700, 64, 10], mutate=_zero_pages, seed=2)
+    check("f32", 8, 2, 64, [700, 64, 10], top_k=50, mutate=_zero_pages, seed=2)
+
+
+def test_all_values_zero():
+    def zero(rng, pools, table, n_slots, listed):
+        pools[3][:] = 0.0
+    check("bf16", 8, 2, 128, [700, 64, 10], mutate=zero, seed=2)
+
+
+def _nan_behind(rng, pools, table, n_slots, listed):
+    """NaN codes, and NaN and infinite scales, everywhere no row looks."""
+    k, v, ks, vs = pools
+    seen = np.zeros((len(k), 64), bool)
+    used = np.zeros(len(k), bool)
+    for b in range(len(table)):
+        for r in range(n_slots.shape[1]):
+            i = np.arange(n_slots[b, r]) if listed is None else listed[b, r][listed[b, r] >= 0]
+            seen[table[b, i // 64], i % 64] = True
+            used[table[b, i // 64]] = True
+    k[~seen] = 0x7f
+    v[~seen] = 0xff
+    ks[~used], vs[~used] = np.nan, np.inf
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,top_k", [(1, 0), (3, 0), (1, 40), (2, 40)])
+def test_nan_outside_the_set(dtype, rows, top_k):
+    check(dtype, 8, 2, 128, [700, 64, 10, 0, 65], rows=rows, top_k=top_k, mutate=_nan_behind, seed=9)
+
+
+@pytest.mark.parametrize("heads,kvh,rows", [(8, 2, 4), (64, 1, 4), (16, 2, 2)])
+def test_nan_that_only_later_rows_see(heads, kvh, rows):
+    """A NaN key or value in a slot that the last rows see and the first do not: only the rows
+    that see it turn NaN (a NaN value only its dimension)."""
+    for which in (0, 1):
+        def one(rng, pools, table, n_slots, listed):
+            i = int(n_slots[0, -1]) - 1
+            pools[which][table[0, i // 64], i % 64, 0, 5] = 0x7f
+        check("bf16", heads, kvh, 128, [130, 64], rows=rows, mutate=one, seed=1)
+
+
+def test_nan_inside_the_set():
+    for which in (0, 1):
+        def one(rng, pools, table, n_slots, listed):
+            pools[which][table[0, 0], 3, 1, 7] = 0xff
+        check("bf16", 8, 2, 128, [130, 64], mutate=one, seed=1)
+        check("f32", 8, 2, 64, [130, 64], mutate=one, seed=1)
+
+
+def test_unordered_and_repeated_list_entries():
+    rng = np.random.default_rng(0)
+    listed = rng.integers(-1, 500, (2, 2, 300)).astype(np.int32)
+    listed[0, 1] = 17                  # one slot 300 times
+    listed[1, 0] = -1                  # nothing
+    check("bf16", 16, 2, 128, [500, 500], rows=2, n_slots=np.full((2, 2), 500), listed=listed, top_k=300)
+
+
+def test_bad_lengths_pages_and_entries_are_reported_and_left_out():
+    check("bf16", 8, 2, 64, [100, 70, 30], n_slots=[[101], [-1], [30]], status_bits=spin.STATUS_BITS["BAD_N"])
+
+    def lost_pages(rng, pools, table, n_slots, listed):
+        table[0, 0], table[1, 1] = -1, 1000
+    for top_k in (0, 90):
+        check("bf16", 8, 2, 64, [100, 70, 30], mutate=lost_pages, top_k=top_k,
+              status_bits=spin.STATUS_BITS["BAD_PAGE"])
+    listed = np.tile(np.array([0, 5, 100, -2, 2 ** 30, -2 ** 31], np.int32), (2, 1, 1))
+    check("bf16", 8, 2, 64, [100, 70], listed=listed, top_k=6, status_bits=spin.STATUS_BITS["BAD_LIST"])
+
+
+def test_pool_beyond_32_bit_offsets():
+    """Pages whose byte offset passes 2^32."""
+    n_pages, kvh, d = 70000, 8, 128
+    k, v = (torch.zeros((n_pages, 64, kvh, d), dtype=torch.uint8, device="cuda") for _ in range(2))
+    rng = np.random.default_rng(0)
+    pages = np.array([[69999, 3, 66001, 68000, 69998]], np.int32)
+    small = _kv.make_pools(rng, 5, kvh, d)
+    for i, p in enumerate(pages[0]):
+        k[int(p)], v[int(p)] = _kv.dev(small[0][i]), _kv.dev(small[1][i])
+    ks, vs = (torch.zeros((n_pages, kvh), device="cuda") for _ in range(2))
+    ks[pages[0].tolist()], vs[pages[0].tolist()] = _kv.dev(small[2]), _kv.dev(small[3])
+    q = torch.from_numpy(rng.normal(size=(1, 1, 16, d))).to(torch.bfloat16)
+    cfg = spin.make_kv_config(1, 320, 1, 16, kvh, d, "bf16")
+    n = np.array([[300]], np.int32)
+    out, _ = _kv.run_attend(cfg, q.cuda(), (k, v, ks, vs), _kv.dev(pages), _kv.dev(n), 1)
+    ref, _, info = o.attend(q.double().numpy(), *small, np.arange(5)[None], n, cfg.softmax_scale)
+    tol, _ = _kv.attend_tolerance("bf16", d, ref, info)
+    assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
+
+
+def test_streams_graphs_and_guard_bands():
+    """The same bits on a side stream, in a replayed graph and from run to run; nothing written
+    around the outputs."""
+    rng = np.random.default_rng(3)
+    lens = [2000, 100, 0, 7]
+    pools = _kv.make_pools(rng, 40, 2, 128)
+    table = _kv.make_table(rng, lens, 40)
+    cfg = spin.make_kv_config(4, 2000, 1, 16, 2, 128, "bf16")
+    dv, dt, dn = [_kv.dev(x) for x in pools], _kv.dev(table), _kv.dev(np.array(lens, np.int32)[:, None])
+    q = torch.from_numpy(rng.normal(size=(4, 1, 16, 128))).to(torch.bfloat16).cuda()
+    want, wlse = _kv.run_attend(cfg, q, dv, dt, dn, 1)
+    for _ in range(3):
+        out, lse = _kv.run_attend(cfg, q, dv, dt, dn, 1)
+        assert torch.equal(out, want) and torch.equal(lse, wlse)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out, lse = _kv.run_attend(cfg, q, dv, dt, dn, 1)
+    side.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, wlse)
+    band = torch.full((q.numel() + 256,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = band[128:-128].view(q.shape)
+    ws = spin.kv_workspace(cfg)
+    g = torch.cuda.CUDAGraph()
+    lse = torch.zeros((4, 1, 16), device="cuda")
+    with torch.cuda.graph(g):
+        spin.kv_attend(cfg, q, *dv, dt, dn, 1, None, out, lse, ws, None)
+    for fill in (0, 255):
+        ws.fill_(fill)
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, wlse)
+    assert (band[:128] == 7).all() and (band[-128:] == 7).all()
