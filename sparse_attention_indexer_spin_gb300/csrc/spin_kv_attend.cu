@@ -3,98 +3,866 @@
 // Per query row and head, over the row's set of slots (its context, or the slots of a list):
 //   s_i = softmax_scale ks (q . kc_i),  out = sum_i e^{s_i} vs vc_i / sum_i e^{s_i},
 //   lse = ln sum_i e^{s_i}
-// in one pass, with the running maximum and sum of the softmax.
+// in one pass over the cache, with the running maximum and sum of the softmax.
+//
+// Numbers.  Everything is in base 2: t_i = log2(e) s_i.  A row keeps a reference m and
+//   l = sum_i 2^(t_i - m),   o = sum_i 2^(t_i - m) vs_i vc_i,   out = o / l
+// in fp32.  Codes become f16 exactly.  q is scaled by a power of two per row to just below 2^15
+// and rounded to f16: bf16 and f16 values keep every bit unless they are below 2^-29 of the
+// row's largest (f16's subnormals; off by at most 2^-39 of it).  The weights 2^(t_i - m) vs_i
+// are rounded to f16 for their product with the codes (2^-11 each).  fp32 queries and
+// weights go in as two f16 terms (22 bits).  The reference follows max(t_i + log2 vs_i) - 12, so
+// that the largest weights, value scale included, sit between 2^12 and 2^15: a page's small
+// value scale costs no precision, and weights lose bits only below 2^-26 of the largest.  The
+// reference moves only when a maximum exceeds it by more than 2^3, which spares most of the
+// rescaling of o.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+
+#include <type_traits>
 
 #include "spin_common.cuh"
 #include "spin_internal.h"
 
 namespace spin {
 
+constexpr int kAtWarps = 4;      // warps of a CTA: each takes every fourth tile of a segment
+constexpr int kAtThreads = 32 * kAtWarps;
+constexpr int kAtTile = 32;      // slots a warp works on at a time
+constexpr int kAtStages = 2;     // tiles in a warp's ring
+constexpr float kAtTop = 12.0f;  // log2 of the largest weight when the reference is set
+constexpr float kAtSlack = 3.0f; // a maximum may exceed that by this much before the reference moves
+constexpr int kAtUnit = 64;      // slots in a unit of work
+constexpr int kAtMinUnits = 2;   // units a CTA takes at least: a tile for each of its warps
+// A job (request or request row, key/value head, chunk of query rows) is split over CTAs
+// unless whole jobs cost at most this many units more on the busiest CTA; the combining
+// launch costs about as much.
+constexpr int kAtSplitGain = 12;
+
+// ------------------------------------------------------------------------ small helpers
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Four e4m3 codes as two pairs of f16 (exact).
+__device__ __forceinline__ void codes_to_f16(uint32_t c, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(c));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+
+__device__ __forceinline__ float2 unpack_f16(uint32_t u) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+
+// D += A B, A 16 x 16 row-major, B 16 x 8 column-major, f16 in, fp32 sums.
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint4 a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+// 16 (or 4) bytes global -> shared, zeros instead where !live.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+
 template <typename T> __device__ __forceinline__ float to_f(T x);
 template <> __device__ __forceinline__ float to_f(float x) { return x; }
 template <> __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 template <> __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-template <typename T> __device__ __forceinline__ T from_f(float x);
-template <> __device__ __forceinline__ float from_f(float x) { return x; }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
-template <> __device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
 
-__device__ __forceinline__ float code_value(uint8_t c) {
-    const __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);
-    return __half2float(*reinterpret_cast<const __half*>(&h));
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__half* p, float4 v) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_f16(v.x, v.y), pack_f16(v.z, v.w));
+}
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// One warp per (request, row, head): lane l holds dims l, l + 32, ...
-template <typename T>
-__global__ void __launch_bounds__(32) kv_attend_kernel(spin_kv_config cfg, KvAttendArgs a) {
-    pdl_begin();
-    const int lane = threadIdx.x, h = blockIdx.x, row = blockIdx.y, b = blockIdx.z;
-    const int H = cfg.n_heads, kvh = cfg.kv_heads, d = cfg.head_dim, g = h / (H / kvh);
-    const int64_t br = (int64_t)b * a.rows + row;
-    int n = a.n_slots[br];
-    if (n < 0 || n > cfg.max_slots) {
-        if (lane == 0) set_status(a.status, SPIN_STATUS_BAD_N);
-        n = 0;
+// -------------------------------------------------------------------- shared-memory tiles
+// A tile is 32 rows (slots) of D bytes in lines of 128 bytes, 16-byte chunk x of row `row` at
+// the position below.  The swizzles make both fragment reads free of bank conflicts: keys are read
+// by quads (four neighbouring chunks of one row, eight rows a warp), values by one chunk of every
+// second row.
+template <int D> __device__ __forceinline__ uint32_t key_at(int row, int x) {
+    if constexpr (D == 64) return (uint32_t)(row * 64 + x * 16);
+    else return (uint32_t)(row * D + (x >> 3) * 128 + (((x & 7) ^ ((row & 1) << 2)) << 4));
+}
+template <int D> __device__ __forceinline__ uint32_t value_at(int row, int x) {
+    if constexpr (D == 64) return (uint32_t)((row >> 1) * 128 + (((((row & 1) << 2) | x) ^ (row & 6)) << 4));
+    else return (uint32_t)(row * D + (x >> 3) * 128 + (((x & 7) ^ (row & 6)) << 4));
+}
+
+template <int D> struct AtStage {  // byte offsets in a stage
+    static constexpr int kValues = kAtTile * D, kKs = 2 * kAtTile * D, kVs = kKs + 4 * kAtTile, kMask = kVs + 4 * kAtTile;
+    static constexpr int kBytes = kMask + 128;
+};
+
+template <int D, int MT, bool SPLIT> struct AtSmem {
+    static constexpr int kRows = 16 * MT;
+    static constexpr int kRing = kAtWarps * kAtStages * AtStage<D>::kBytes;
+    static constexpr int kMerge = kAtWarps * kRows * D * 4;          // shares the ring's memory
+    static constexpr int kMain = kRing > kMerge ? kRing : kMerge;
+    static constexpr int kQ = MT * (SPLIT ? 2 : 1) * (D / 16) * 512;  // query fragments
+    static constexpr int kBytes = kMain + kQ + kRows * 8 + 2 * kAtWarps * kRows * 4 + kAtThreads * 8 + 64;
+};
+
+// Merged rows in shared memory: float4 f of a row is kept at f ^ rot, so that the eight lanes of
+// a store phase (two rows, four column groups) hit different banks.
+template <int D> __device__ __forceinline__ int merge_at(int row, int f) {
+    if constexpr (D == 64) return (f & ~3) | ((f & 3) ^ (((f >> 3) & 1) + 2 * (row & 1)));
+    else return (f & ~7) | ((f & 7) ^ (((f >> 3) & 3) + 4 * (row & 1)));
+}
+
+// ------------------------------------------------------------------------- work division
+struct AtPlan {
+    int split;      // jobs may be divided over CTAs
+    int mchunks;    // chunks of query rows per key/value head
+    int n_virtual;  // requests, or with lists request rows
+    float* rec;     // partial results: two records per CTA
+    int4* owner;    // per CTA: job it begins and does not finish, and the number of pieces
+};
+
+// Slots of request b's longest row (its own row's with a list); bad lengths count as 0.
+__device__ __forceinline__ int row_slots(const KvAttendArgs& a, int64_t br, int max_slots) {
+    const int n = a.n_slots[br];
+    if (n < 0 || n > max_slots) {
+        set_status(a.status, SPIN_STATUS_BAD_N);
+        return 0;
     }
-    float q[8], o[8];
+    return n;
+}
+
+template <bool SPARSE>
+__device__ __forceinline__ int virtual_len(const spin_kv_config& cfg, const KvAttendArgs& a, int v) {
+    if constexpr (SPARSE) {
+        return row_slots(a, v, cfg.max_slots) > 0 ? a.top_k : 0;
+    } else {
+        int n = 0;
+        for (int r = 0; r < a.rows; ++r) n = max(n, row_slots(a, (int64_t)v * a.rows + r, cfg.max_slots));
+        return n;
+    }
+}
+
+__device__ __forceinline__ int64_t warp_incl_scan64(int64_t v) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int c = lane + 32 * i;
-        q[i] = c < d ? to_f(reinterpret_cast<const T*>(a.q)[(br * H + h) * d + c]) * cfg.softmax_scale : 0.0f;
-        o[i] = 0.0f;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += t;
     }
+    return v;
+}
+
+// Inclusive scan over the CTA; *total is the sum.
+__device__ __forceinline__ int64_t cta_incl_scan64(int64_t v, int64_t* smem, int64_t* total) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int64_t s = warp_incl_scan64(v);
+    if (lane == 31) smem[w] = s;
+    __syncthreads();
+    int64_t all = 0;
+#pragma unroll
+    for (int i = 0; i < kAtWarps; ++i) {
+        if (i < w) s += smem[i];
+        all += smem[i];
+    }
+    __syncthreads();
+    *total = all;
+    return s;
+}
+
+// --------------------------------------------------------------------------- the kernel
+template <typename T, int D, int MT, bool SPARSE>
+__global__ void __launch_bounds__(kAtThreads, D == 256 ? 1 : 2)
+kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_constant__ KvAttendArgs a, AtPlan plan) {
+    pdl_begin();
+    constexpr bool SPLIT = std::is_same<T, float>::value;
+    constexpr bool QREG = MT == 1 && !SPLIT && D <= 128;  // query fragments stay in registers
+    using L = AtSmem<D, MT, SPLIT>;
+    using St = AtStage<D>;
+    constexpr int NT = D / 8;       // column tiles of o
+    constexpr int KS = D / 16;      // contraction steps of q . k
+    extern __shared__ __align__(128) unsigned char smem[];
+    uint4* sQ = reinterpret_cast<uint4*>(smem + L::kMain);
+    float* sQs = reinterpret_cast<float*>(smem + L::kMain + L::kQ);
+    int* sN = reinterpret_cast<int*>(sQs + L::kRows);
+    float* sM = reinterpret_cast<float*>(sN + L::kRows);
+    float* sL = sM + kAtWarps * L::kRows;
+    int64_t* sScan = reinterpret_cast<int64_t*>(sL + kAtWarps * L::kRows);
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
+    const int H = cfg.n_heads, kvh = cfg.kv_heads, d = cfg.head_dim, group = H / kvh;
+    const int rows = SPARSE ? 1 : a.rows, M = group * rows;
+    const int me = blockIdx.x;
+    int64_t G = gridDim.x;  // CTAs with work, once the work is known
+    const int64_t per_request = (int64_t)kvh * plan.mchunks;
     const float ninf = __uint_as_float(0xff800000u);
-    float m = ninf, l = 0.0f;
-    const int cnt = a.list ? a.top_k : n;
-    for (int t = 0; t < cnt; ++t) {
-        int i = t;
-        if (a.list) {
-            i = a.list[br * a.top_k + t];
-            if (i == -1) continue;
-            if (i < 0 || i >= n) {
-                if (lane == 0) set_status(a.status, SPIN_STATUS_BAD_LIST);
-                continue;
+
+    // requests without any slot: zeros
+    for (int v = me; v < plan.n_virtual; v += gridDim.x) {
+        if (virtual_len<SPARSE>(cfg, a, v) > 0) continue;
+        const int64_t base = (int64_t)v * rows * H;
+        for (int64_t e = tid; e < (int64_t)rows * H * d / 4; e += kAtThreads)
+            store4(reinterpret_cast<T*>(a.out) + base * d + 4 * e, make_float4(0, 0, 0, 0));
+        if (a.lse)
+            for (int e = tid; e < rows * H; e += kAtThreads) a.lse[base + e] = ninf;
+    }
+
+    // this CTA's part of the work: units [begin, end) of all jobs laid end to end (split), or
+    // jobs me, me + G, ... whole
+    int64_t total = 0, begin = 0, end = 0;
+    int v = 0;          // request the part begins in
+    int64_t into = 0;   // units of that request before it
+    if (plan.split) {
+        for (int base = 0; base < plan.n_virtual; base += kAtThreads) {
+            const int x = base + tid;
+            const int64_t u = x < plan.n_virtual ? (virtual_len<SPARSE>(cfg, a, x) + kAtUnit - 1) / kAtUnit : 0;
+            int64_t sum;
+            cta_incl_scan64(u * per_request, sScan, &sum);
+            total += sum;
+        }
+        // every CTA that takes part has a unit at least: a divided job's pieces are those of
+        // consecutive CTAs
+        G = min(G, (total + kAtMinUnits - 1) / kAtMinUnits);
+        if (me < G) {
+            begin = total * me / G;
+            end = total * (me + 1) / G;
+        }
+        if (begin < end) {
+            int64_t before = 0;
+            if (tid == 0) sScan[8] = -1;
+            for (int base = 0; base < plan.n_virtual; base += kAtThreads) {
+                const int x = base + tid;
+                const int64_t u = x < plan.n_virtual ? (virtual_len<SPARSE>(cfg, a, x) + kAtUnit - 1) / kAtUnit : 0;
+                int64_t sum;
+                const int64_t inc = before + cta_incl_scan64(u * per_request, sScan, &sum);
+                if (inc > begin && inc - u * per_request <= begin) {
+                    sScan[8] = x;
+                    sScan[9] = inc - u * per_request;
+                }
+                before += sum;
+                if (before > begin) break;
+            }
+            __syncthreads();
+            v = (int)sScan[8];
+            into = begin - sScan[9];
+        }
+        if (tid == 0) plan.owner[me] = make_int4(-1, 0, 0, 0);
+    }
+
+    int64_t job = me;   // whole jobs
+    for (int64_t at = begin;;) {
+        // ---- the next segment: job (v, g, mc), units [u0, u1) of its `units`
+        int g, mc, len, units, u0, u1;
+        if (plan.split) {
+            if (at >= end) break;
+            for (;;) {
+                len = virtual_len<SPARSE>(cfg, a, v);
+                units = (len + kAtUnit - 1) / kAtUnit;
+                if (into < units * per_request) break;
+                into = 0;
+                ++v;
+            }
+            const int64_t j = into / units;
+            g = (int)(j / plan.mchunks);
+            mc = (int)(j % plan.mchunks);
+            u0 = (int)(into % units);
+            u1 = (int)min((int64_t)units, u0 + (end - at));
+        } else {
+            if (job >= plan.n_virtual * per_request) break;
+            v = (int)(job / per_request);
+            g = (int)(job % per_request / plan.mchunks);
+            mc = (int)(job % plan.mchunks);
+            job += G;
+            len = virtual_len<SPARSE>(cfg, a, v);
+            if (len == 0) continue;
+            units = (len + kAtUnit - 1) / kAtUnit;
+            u0 = 0;
+            u1 = units;
+        }
+        const int64_t b = SPARSE ? v / a.rows : v;
+        const int64_t br0 = SPARSE ? v : (int64_t)v * a.rows;  // first (request, row)
+        const int m0 = mc * L::kRows, mrows = min(L::kRows, M - m0);
+
+        // ---- queries: row m is (row m / group, head g * group + m % group), scaled by a power
+        // of two and rounded to f16, laid out as the fragments read them
+        for (int m = wid; m < L::kRows; m += kAtWarps) {
+            const int64_t br = br0 + (m0 + m) / group;
+            const T* qp = reinterpret_cast<const T*>(a.q) + (br * H + (int64_t)g * group + (m0 + m) % group) * d;
+            float x[D / 32], amax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const int c = lane * (D / 32) + i;
+                x[i] = m < mrows && c < d ? to_f(qp[c]) : 0.0f;
+                amax = fmaxf(amax, fabsf(x[i]));
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            // amax in [2^k, 2^(k+1)) -> [2^14, 2^15); 2^(14 - k) within [2^-113, 2^126]
+            const int k = max(-112, (int)(__float_as_uint(amax) >> 23) - 127);
+            const float f = __uint_as_float((uint32_t)(127 + 14 - k) << 23);
+            if (lane == 0) {
+                sQs[m] = __uint_as_float((uint32_t)max(1, 127 - 14 + k) << 23) * (cfg.softmax_scale * 1.4426950408889634f);
+                int n = 0x7fffffff;
+                if (!SPARSE && m < mrows) n = row_slots(a, br, cfg.max_slots);
+                sN[m] = n;
+            }
+            // dims 64c + 16t + 4s + {0, 1} of row m are the pair k = 2t of contraction step 4c + s,
+            // {2, 3} the pair k = 2t + 8
+#pragma unroll
+            for (int i = 0; i < D / 32; i += 2) {
+                const int c = lane * (D / 32) + i;
+                const uint32_t hi = pack_f16(x[i] * f, x[i + 1] * f);
+                const int step = (c >> 6) * 4 + ((c >> 2) & 3), t = (c >> 4) & 3, pair = (c >> 1) & 1;
+                const int word = ((m & 15) >> 3) + 2 * pair, ln = (m & 7) * 4 + t;
+                uint32_t* at32 = reinterpret_cast<uint32_t*>(sQ) + (((m >> 4) * KS + step) * 32 + ln) * 4 + word;
+                *at32 = hi;
+                if constexpr (SPLIT) {
+                    const float2 h = unpack_f16(hi);
+                    at32[MT * KS * 128] = pack_f16(x[i] * f - h.x, x[i + 1] * f - h.y);
+                }
             }
         }
-        const int64_t page = a.block_table[(int64_t)b * a.bt_stride + (i >> 6)];
-        if (page < 0 || page >= a.n_pages) {
-            if (lane == 0) set_status(a.status, SPIN_STATUS_BAD_PAGE);
-            continue;
+        __syncthreads();
+        uint4 qr[QREG ? KS : 1];
+        if constexpr (QREG) {
+#pragma unroll
+            for (int s = 0; s < KS; ++s) qr[s] = sQ[s * 32 + lane];
         }
-        const int64_t at = ((page * kBlock + (i & 63)) * kvh + g) * d;
-        float s = 0.0f;
+        float qs[MT][2];
+        int nlim[MT][2], nmin = 0x7fffffff;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (lane + 32 * k < d) s = fmaf(q[k], code_value(a.k_pool[at + lane + 32 * k]), s);
+        for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= a.k_scale[page * kvh + g];
-        const float vs = a.v_scale[page * kvh + g];
-        const float mn = fmaxf(m, s), f = m == ninf ? 0.0f : expf(m - mn), p = expf(s - mn);
-        m = mn;
-        l = l * f + p;
+            for (int x = 0; x < 2; ++x) {
+                qs[i][x] = sQs[16 * i + 8 * x + g8];
+                nlim[i][x] = sN[16 * i + 8 * x + g8];
+                nmin = min(nmin, nlim[i][x]);
+            }
+        nmin = __reduce_min_sync(0xffffffffu, nmin);
+
+        float o[MT][NT][4], mx[MT][2], lsum[MT][2];
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (lane + 32 * k < d) o[k] = o[k] * f + p * vs * code_value(a.v_pool[at + lane + 32 * k]);
+        for (int i = 0; i < MT; ++i) {
+            mx[i][0] = mx[i][1] = ninf;
+            lsum[i][0] = lsum[i][1] = 0.0f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.0f;
+        }
+
+        // ---- this warp's tiles: tile0 + wid, + kAtWarps, ... below tile1
+        const int tile0 = u0 * (kAtUnit / kAtTile), tile1 = min(u1 * (kAtUnit / kAtTile), (len + kAtTile - 1) / kAtTile);
+        const int nt = max(0, (tile1 - tile0 - wid + kAtWarps - 1) / kAtWarps);
+        const uint32_t ring = smem_u32(smem) + (uint32_t)(wid * kAtStages * St::kBytes);
+        const int32_t* table = a.block_table + b * a.bt_stride;
+        const int row_n = SPARSE ? row_slots(a, br0, cfg.max_slots) : 0;
+        const int64_t row_bytes = (int64_t)kvh * d;
+
+        // Entries and pages are read ahead of the copies that need them: a list entry two tiles, a
+        // page one tile.
+        auto entry = [&](int k) -> int {  // slot of this lane in the warp's k-th tile, -1: none
+            const int t = tile0 + wid + k * kAtWarps;
+            if constexpr (SPARSE) {
+                const int e = t * kAtTile + lane;
+                if (k >= nt || e >= a.top_k) return -1;
+                const int i = a.list[(int64_t)v * a.top_k + e];
+                if (i >= 0 && i < row_n) return i;
+                if (i != -1) set_status(a.status, SPIN_STATUS_BAD_LIST);
+                return -1;
+            } else {
+                const int i = t * kAtTile + lane;
+                return k < nt && i < len ? i : -1;
+            }
+        };
+        auto page_at = [&](int i) -> int {
+            if (i < 0) return -1;
+            const int p = table[i >> 6];
+            if (p >= 0 && p < a.n_pages) return p;
+            set_status(a.status, SPIN_STATUS_BAD_PAGE);
+            return -1;
+        };
+        int e_now = entry(0), e_next = entry(1), p_now = page_at(e_now);
+
+        auto issue = [&](int k) {  // the k-th tile's copies into its stage
+            if (k < nt) {
+                const uint32_t st = ring + (uint32_t)((k % kAtStages) * St::kBytes);
+                const bool live = p_now >= 0;
+                const int64_t off = live ? ((int64_t)p_now * kBlock + (e_now & 63)) * row_bytes + (int64_t)g * d : 0;
+                const int64_t so = live ? (int64_t)p_now * kvh + g : 0;
+                constexpr int CH = D / 16;  // chunks of a row
+#pragma unroll
+                for (int i = 0; i < CH; ++i) {
+                    const int row = (lane + 32 * i) / CH, x = lane % CH;
+                    const int64_t ro = __shfl_sync(0xffffffffu, off, row) + 16 * x;
+                    const bool ok = __shfl_sync(0xffffffffu, (int)live, row) && 16 * x < d;
+                    cp16(st + key_at<D>(row, x), a.k_pool + (ok ? ro : 0), ok);
+                    cp16(st + St::kValues + value_at<D>(row, x), a.v_pool + (ok ? ro : 0), ok);
+                }
+                cp4(st + St::kKs + 4 * lane, a.k_scale + so, live);
+                cp4(st + St::kVs + 4 * lane, a.v_scale + so, live);
+                const uint32_t mask = __ballot_sync(0xffffffffu, live);
+                if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + St::kMask), "r"(mask) : "memory");
+                e_now = e_next;
+                p_now = page_at(e_now);
+                e_next = entry(k + 2);
+            }
+            cp_commit();
+        };
+#pragma unroll
+        for (int k = 0; k < kAtStages; ++k) issue(k);
+
+        for (int k = 0; k < nt; ++k) {
+            cp_wait<kAtStages - 1>();
+            __syncwarp();
+            const uint32_t st = ring + (uint32_t)((k % kAtStages) * St::kBytes);
+            const int slot0 = (tile0 + wid + k * kAtWarps) * kAtTile;
+            uint32_t mask;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(mask) : "r"(st + St::kMask) : "memory");
+
+            // ---- scores of 32 slots: column tile j holds slots 8j ..
+            float s[MT][4][4];
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[i][j][0] = s[i][j][1] = s[i][j][2] = s[i][j][3] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                uint4 qf[QREG ? 1 : MT * (SPLIT ? 2 : 1)][QREG ? 1 : 4];
+                if constexpr (!QREG) {
+#pragma unroll
+                    for (int i = 0; i < MT * (SPLIT ? 2 : 1); ++i)
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) qf[i][w] = sQ[(i * KS + 4 * c + w) * 32 + lane];
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint4 kc = lds128(st + key_at<D>(8 * j + g8, 4 * c + t4));
+                    const uint32_t kw[4] = {kc.x, kc.y, kc.z, kc.w};
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        uint32_t b0, b1;
+                        codes_to_f16(kw[w], b0, b1);
+                        if constexpr (QREG) {
+                            mma_f16(s[0][j], qr[4 * c + w], b0, b1);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < MT; ++i) {
+                                mma_f16(s[i][j], qf[i][w], b0, b1);
+                                if constexpr (SPLIT) mma_f16(s[i][j], qf[MT + i][w], b0, b1);
+                            }
+                        }
+                    }
+                }
+            }
+
+            // ---- weights
+            float ks[8], vs[8], lv[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint2 x = lds64(st + St::kKs + 4 * (8 * j + 2 * t4)), y = lds64(st + St::kVs + 4 * (8 * j + 2 * t4));
+                ks[2 * j] = __uint_as_float(x.x);
+                ks[2 * j + 1] = __uint_as_float(x.y);
+                vs[2 * j] = __uint_as_float(y.x);
+                vs[2 * j + 1] = __uint_as_float(y.y);
+                lv[2 * j] = fmaxf(lg2(fabsf(vs[2 * j])), -100.0f);
+                lv[2 * j + 1] = fmaxf(lg2(fabsf(vs[2 * j + 1])), -100.0f);
+            }
+            const bool border = mask != 0xffffffffu || slot0 + kAtTile > nmin;
+            float top[MT][2];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                top[i][0] = top[i][1] = ninf;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int col = 2 * j + (x & 1), r = x >> 1;
+                        float y = s[i][j][x] * qs[i][r] * ks[col];
+                        if (border) {
+                            const int at_slot = 8 * j + 2 * t4 + (x & 1);
+                            if (!((mask >> at_slot) & 1u) || slot0 + at_slot >= nlim[i][r]) y = ninf;
+                        }
+                        s[i][j][x] = y;
+                        top[i][r] = fmaxf(top[i][r], y + lv[col]);
+                    }
+            }
+            bool move = false;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    top[i][r] = fmaxf(top[i][r], __shfl_xor_sync(0xffffffffu, top[i][r], 1));
+                    top[i][r] = fmaxf(top[i][r], __shfl_xor_sync(0xffffffffu, top[i][r], 2)) - kAtTop;
+                    move |= top[i][r] > mx[i][r] + kAtSlack;
+                }
+            if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float now = fmaxf(mx[i][r], top[i][r]);
+                        const float f = now == ninf ? 1.0f : ex2(mx[i][r] - now);
+                        mx[i][r] = now;
+                        lsum[i][r] *= f;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            o[i][n][2 * r] *= f;
+                            o[i][n][2 * r + 1] *= f;
+                        }
+                    }
+            }
+            uint4 pw[MT][SPLIT ? 2 : 1][2];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const float ref0 = mx[i][0] == ninf ? 0.0f : mx[i][0], ref1 = mx[i][1] == ninf ? 0.0f : mx[i][1];
+                uint32_t ph[8], pl[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float p[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        p[x] = ex2(s[i][j][x] - ((x >> 1) ? ref1 : ref0));
+                        lsum[i][x >> 1] += p[x];
+                        p[x] *= vs[2 * j + (x & 1)];
+                    }
+                    ph[2 * j] = pack_f16(p[0], p[1]);
+                    ph[2 * j + 1] = pack_f16(p[2], p[3]);
+                    if constexpr (SPLIT) {
+                        const float2 h0 = unpack_f16(ph[2 * j]), h1 = unpack_f16(ph[2 * j + 1]);
+                        pl[2 * j] = pack_f16(p[0] - h0.x, p[1] - h0.y);
+                        pl[2 * j + 1] = pack_f16(p[2] - h1.x, p[3] - h1.y);
+                    }
+                }
+                pw[i][0][0] = make_uint4(ph[0], ph[1], ph[2], ph[3]);
+                pw[i][0][1] = make_uint4(ph[4], ph[5], ph[6], ph[7]);
+                if constexpr (SPLIT) {
+                    pw[i][1][0] = make_uint4(pl[0], pl[1], pl[2], pl[3]);
+                    pw[i][1][1] = make_uint4(pl[4], pl[5], pl[6], pl[7]);
+                }
+            }
+
+            // A NaN code that some rows see and others do not would reach the others as 0 x NaN:
+            // such codes turn the outputs of the rows that see them to NaN here and leave the tile.
+            if (!SPARSE && rows > 1 && slot0 + kAtTile > nmin) {
+                bool nan = false;
+                for (int e = lane; e < kAtTile * D / 4; e += 32) {
+                    uint32_t w;
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(st + St::kValues + 4 * e) : "memory");
+                    w &= 0x7f7f7f7fu;
+                    nan |= ((w + 0x01010101u) & 0x80808080u) != 0;
+                }
+                if (__any_sync(0xffffffffu, nan)) {
+                    for (int sl = 0; sl < kAtTile; ++sl) {
+                        const int slot = slot0 + sl;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const int dim = D == 64 ? 8 * (2 * t4 + x) + n
+                                                        : 128 * (n >> 4) + 16 * (2 * t4 + x) + (n & 15);
+                                uint32_t c;
+                                asm volatile("ld.shared.u8 %0, [%1];"
+                                             : "=r"(c)
+                                             : "r"(st + St::kValues + value_at<D>(sl, dim >> 4) + (dim & 15))
+                                             : "memory");
+                                if ((c & 0x7fu) != 0x7fu) continue;
+#pragma unroll
+                                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                                    for (int r = 0; r < 2; ++r)
+                                        if (slot < nlim[i][r]) o[i][n][2 * r + x] = __uint_as_float(0x7fffffffu);
+                            }
+                    }
+                    __syncwarp();
+                    for (int e = lane; e < kAtTile * D; e += 32) {
+                        uint32_t c;
+                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(c) : "r"(st + St::kValues + e) : "memory");
+                        if ((c & 0x7fu) == 0x7fu)
+                            asm volatile("st.shared.u8 [%0], %1;" ::"r"(st + St::kValues + e), "r"(0) : "memory");
+                    }
+                    __syncwarp();
+                }
+            }
+
+            // ---- o += weights x values: column n of tile i holds dim 16 n + i (of each 128; D = 64:
+            // 8 n + i)
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+                const int r0 = 16 * kk + 2 * t4;
+                constexpr int HALVES = D == 64 ? 1 : D / 128, WORDS = D == 64 ? 2 : 4;
+#pragma unroll
+                for (int hh = 0; hh < HALVES; ++hh) {
+                    uint32_t vw[4][4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int row = r0 + (q & 1) + 8 * (q >> 1);
+                        if constexpr (D == 64) {
+                            const uint2 x = lds64(st + St::kValues + value_at<D>(row, g8 >> 1) + 8 * (g8 & 1));
+                            vw[q][0] = x.x;
+                            vw[q][1] = x.y;
+                        } else {
+                            const uint4 x = lds128(st + St::kValues + value_at<D>(row, g8 + 8 * hh));
+                            vw[q][0] = x.x;
+                            vw[q][1] = x.y;
+                            vw[q][2] = x.z;
+                            vw[q][3] = x.w;
+                        }
+                    }
+#pragma unroll
+                    for (int w = 0; w < WORDS; ++w) {
+                        uint32_t b0[4], b1[4];
+                        codes_to_f16(__byte_perm(vw[0][w], vw[1][w], 0x5140), b0[0], b0[1]);
+                        codes_to_f16(__byte_perm(vw[0][w], vw[1][w], 0x7362), b0[2], b0[3]);
+                        codes_to_f16(__byte_perm(vw[2][w], vw[3][w], 0x5140), b1[0], b1[1]);
+                        codes_to_f16(__byte_perm(vw[2][w], vw[3][w], 0x7362), b1[2], b1[3]);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+#pragma unroll
+                            for (int i = 0; i < MT; ++i) {
+                                mma_f16(o[i][16 * hh + 4 * w + y], pw[i][0][kk], b0[y], b1[y]);
+                                if constexpr (SPLIT) mma_f16(o[i][16 * hh + 4 * w + y], pw[i][SPLIT][kk], b0[y], b1[y]);
+                            }
+                    }
+                }
+            }
+            __syncwarp();
+            issue(k + kAtStages);
+        }
+        cp_wait<0>();
+        __syncthreads();   // the ring is free: the warps' results go there
+
+        // ---- merge the warps
+        float* sO = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = 16 * i + 8 * r + g8;
+                lsum[i][r] += __shfl_xor_sync(0xffffffffu, lsum[i][r], 1);
+                lsum[i][r] += __shfl_xor_sync(0xffffffffu, lsum[i][r], 2);
+                if (t4 == 0) {
+                    sM[wid * L::kRows + row] = mx[i][r];
+                    sL[wid * L::kRows + row] = lsum[i][r];
+                }
+                float4* dst = reinterpret_cast<float4*>(sO + (wid * L::kRows + row) * D);
+                constexpr int PER = D == 64 ? 8 : 16;  // tiles that one column spans
+#pragma unroll
+                for (int hh = 0; hh < NT / PER; ++hh)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+#pragma unroll
+                        for (int q = 0; q < PER / 4; ++q) {
+                            const int f = 32 * hh + (2 * t4 + x) * (PER / 4) + q, n = PER * hh + 4 * q;
+                            dst[merge_at<D>(row, f)] = make_float4(o[i][n][2 * r + x], o[i][n + 1][2 * r + x],
+                                                                   o[i][n + 2][2 * r + x], o[i][n + 3][2 * r + x]);
+                        }
+            }
+        __syncthreads();
+        const bool whole = u0 == 0 && u1 == units;
+        float* rec = nullptr;
+        if (!whole) rec = plan.rec + (int64_t)(2 * me + (u0 == 0 ? 1 : 0)) * L::kRows * (D + 2);
+        for (int e = tid; e < mrows * (D / 4); e += kAtThreads) {
+            const int m = e / (D / 4), f = e % (D / 4);
+            float top = ninf;
+#pragma unroll
+            for (int w = 0; w < kAtWarps; ++w) top = fmaxf(top, sM[w * L::kRows + m]);
+            float l = 0.0f;
+            float4 acc = make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int w = 0; w < kAtWarps; ++w) {
+                const float mw = sM[w * L::kRows + m];
+                const float c = mw == ninf ? 0.0f : ex2(mw - top);
+                const float4 x = reinterpret_cast<const float4*>(sO + (w * L::kRows + m) * D)[merge_at<D>(m, f)];
+                // a warp without a slot of this row has l = 0 and c = 0; one that saw only NaN scores
+                // has l = NaN, which stays
+                l = fmaf(c, sL[w * L::kRows + m], l);
+                acc.x = fmaf(c, x.x, acc.x);
+                acc.y = fmaf(c, x.y, acc.y);
+                acc.z = fmaf(c, x.z, acc.z);
+                acc.w = fmaf(c, x.w, acc.w);
+            }
+            if (whole) {
+                const int64_t bh = (br0 + (m0 + m) / group) * H + (int64_t)g * group + (m0 + m) % group;
+                const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+                if (l == 0.0f) acc = make_float4(0, 0, 0, 0);
+                if (4 * f < d)
+                    store4(reinterpret_cast<T*>(a.out) + bh * d + 4 * f,
+                           make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+                if (a.lse && f == 0) a.lse[bh] = l == 0.0f ? ninf : ((top == ninf ? 0.0f : top) + log2f(l)) * 0.6931471805599453f;
+            } else {
+                reinterpret_cast<float4*>(rec + m * D)[f] = acc;
+                if (f == 0) {
+                    rec[L::kRows * D + 2 * m] = top;
+                    rec[L::kRows * D + 2 * m + 1] = l;
+                }
+            }
+        }
+        if (plan.split) {
+            if (tid == 0 && u0 == 0 && u1 < units) {
+                // the CTA that holds the job's last unit
+                const int64_t last = at + units - 1;
+                int64_t c = last * G / total;
+                while (total * (c + 1) / G <= last) ++c;
+                while (total * c / G > last) --c;
+                plan.owner[me] = make_int4(v, g, mc, (int)(c - me) + 1);
+            }
+            at += u1 - u0;
+            into += u1 - u0;
+        }
+        __syncthreads();
     }
-    const float inv = m == ninf ? 0.0f : 1.0f / l;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        if (lane + 32 * k < d) reinterpret_cast<T*>(a.out)[(br * H + h) * d + lane + 32 * k] = from_f<T>(o[k] * inv);
-    if (a.lse && lane == 0) a.lse[br * H + h] = m == ninf ? ninf : m + logf(l);
 }
 
-size_t kv_attend_workspace_bytes(const spin_kv_config&, int, int) { return 256; }
+// Joins the pieces of the jobs that were divided: the owner's second record, then the first
+// records of the CTAs after it.  One warp per query row.
+template <typename T, int D, int MT>
+__global__ void __launch_bounds__(256) kv_attend_join_kernel(spin_kv_config cfg, KvAttendArgs a, AtPlan plan, int rows) {
+    pdl_begin();
+    constexpr int ROWS = 16 * MT, REC = ROWS * (D + 2), F = D / 32;
+    const int4 job = plan.owner[blockIdx.x];
+    if (job.x < 0) return;
+    const int lane = threadIdx.x & 31, H = cfg.n_heads, d = cfg.head_dim, group = H / cfg.kv_heads;
+    const int m0 = job.z * ROWS, mrows = min(ROWS, group * rows - m0), pieces = job.w;
+    const float ninf = __uint_as_float(0xff800000u);
+    const float* rec0 = plan.rec + (int64_t)(2 * blockIdx.x + 1) * REC;
+    const float* rec1 = plan.rec + (int64_t)(2 * blockIdx.x + 2) * REC;  // piece p >= 1: rec1 + 2 (p - 1) REC
+    for (int m = threadIdx.x >> 5; m < mrows; m += 8) {
+        float top = ninf;
+        for (int p = lane; p < pieces; p += 32)
+            top = fmaxf(top, (p ? rec1 + (int64_t)2 * (p - 1) * REC : rec0)[ROWS * D + 2 * m]);
+#pragma unroll
+        for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        float l = 0.0f, acc[F];
+#pragma unroll
+        for (int i = 0; i < F; ++i) acc[i] = 0.0f;
+#pragma unroll 8
+        for (int p = 0; p < pieces; ++p) {
+            const float* r = p ? rec1 + (int64_t)2 * (p - 1) * REC : rec0;
+            const float mw = r[ROWS * D + 2 * m];
+            const float c = mw == ninf ? 0.0f : ex2(mw - top);
+            l = fmaf(c, r[ROWS * D + 2 * m + 1], l);
+            float x[F];
+            if constexpr (F == 2) {
+                const float2 y = reinterpret_cast<const float2*>(r + m * D)[lane];
+                x[0] = y.x; x[1] = y.y;
+            } else {
+#pragma unroll
+                for (int i = 0; i < F; i += 4) {
+                    const float4 y = reinterpret_cast<const float4*>(r + m * D)[lane * (F / 4) + i / 4];
+                    x[i] = y.x; x[i + 1] = y.y; x[i + 2] = y.z; x[i + 3] = y.w;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < F; ++i) acc[i] = fmaf(c, x[i], acc[i]);
+        }
+        const int64_t v = job.x;
+        const int64_t bh = (v * rows + (m0 + m) / group) * H + (int64_t)job.y * group + (m0 + m) % group;
+        const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+        T* out = reinterpret_cast<T*>(a.out) + bh * d;
+#pragma unroll
+        for (int i = 0; i < F; ++i) {
+            const int c = lane * F + i;
+            const float y = l == 0.0f ? 0.0f : acc[i] * inv;
+            if (c < d) {
+                if constexpr (std::is_same<T, float>::value) out[c] = y;
+                else if constexpr (std::is_same<T, __half>::value) out[c] = __float2half_rn(y);
+                else out[c] = __float2bfloat16_rn(y);
+            }
+        }
+        if (a.lse && lane == 0) a.lse[bh] = l == 0.0f ? ninf : ((top == ninf ? 0.0f : top) + log2f(l)) * 0.6931471805599453f;
+    }
+}
+
+// ------------------------------------------------------------------------------ host side
+static int at_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
+// one row tile (16 query rows of a key/value head) a warp, two where there are more; a 256-wide
+// output leaves registers for one
+static int at_mtiles(int D, int M) { return M > 16 && D <= 128 ? 2 : 1; }
+
+// At least two CTAs' worth of records for any split launch.
+size_t kv_attend_workspace_bytes(const spin_kv_config& cfg, int, int) {
+    const int D = at_dim(cfg.head_dim);
+    const size_t G = 2 * (size_t)device_sm_count();
+    return (G * sizeof(int4) + 255) / 256 * 256 + G * 2 * 32 * (size_t)(D + 2) * sizeof(float);
+}
+
+template <typename T, int D, int MT, bool SPARSE>
+static cudaError_t launch_at(const spin_kv_config& cfg, const KvAttendArgs& a, cudaStream_t s) {
+    using L = AtSmem<D, MT, std::is_same<T, float>::value>;
+    auto k = kv_attend_kernel<T, D, MT, SPARSE>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+    if (e != cudaSuccess) return e;
+    const int M = cfg.n_heads / cfg.kv_heads * (SPARSE ? 1 : a.rows);
+    AtPlan p;
+    p.mchunks = (M + L::kRows - 1) / L::kRows;
+    p.n_virtual = SPARSE ? cfg.n_req * a.rows : cfg.n_req;
+    const int64_t jobs = (int64_t)p.n_virtual * cfg.kv_heads * p.mchunks;
+    const int64_t most = ((SPARSE ? a.top_k : cfg.max_slots) + kAtUnit - 1) / kAtUnit;
+    const int64_t ctas = (D == 256 ? 1 : 2) * (int64_t)device_sm_count();
+    // whole jobs: ceil(jobs / ctas) * most units on the busiest CTA; split: jobs * most / ctas
+    p.split = (jobs + ctas - 1) / ctas * most > jobs * most / ctas + kAtSplitGain;
+    const int64_t work = p.split ? jobs * ((most + kAtMinUnits - 1) / kAtMinUnits) : jobs;
+    const int G = (int)(work < ctas ? work : ctas);
+    p.owner = reinterpret_cast<int4*>(a.workspace);
+    p.rec = a.workspace + ((size_t)2 * device_sm_count() * sizeof(int4) + 255) / 256 * 64;
+    e = launch_pdl(k, dim3(G), dim3(kAtThreads), L::kBytes, s, nullptr, 0, cfg, a, p);
+    if (e != cudaSuccess || !p.split) return e;
+    return launch_pdl(kv_attend_join_kernel<T, D, MT>, dim3(G), dim3(256), 0, s, nullptr, 0, cfg, a, p,
+                      SPARSE ? 1 : a.rows);
+}
+
+template <typename T, int D, int MT>
+static cudaError_t launch_list(const spin_kv_config& cfg, const KvAttendArgs& a, cudaStream_t s) {
+    return a.list ? launch_at<T, D, MT, true>(cfg, a, s) : launch_at<T, D, MT, false>(cfg, a, s);
+}
+
+template <typename T>
+static cudaError_t launch_typed(const spin_kv_config& cfg, const KvAttendArgs& a, cudaStream_t s) {
+    const int M = cfg.n_heads / cfg.kv_heads * (a.list ? 1 : a.rows), D = at_dim(cfg.head_dim);
+    const int mt = at_mtiles(D, M);
+    if (D == 256) return launch_list<T, 256, 1>(cfg, a, s);
+    if (D == 128) return mt == 1 ? launch_list<T, 128, 1>(cfg, a, s) : launch_list<T, 128, 2>(cfg, a, s);
+    return mt == 1 ? launch_list<T, 64, 1>(cfg, a, s) : launch_list<T, 64, 2>(cfg, a, s);
+}
 
 cudaError_t launch_kv_attend(const spin_kv_config& cfg, const KvAttendArgs& a, cudaStream_t s) {
-    const dim3 grid(cfg.n_heads, a.rows, cfg.n_req);
     switch (cfg.dtype) {
-        case SPIN_DTYPE_F32: return launch_pdl(kv_attend_kernel<float>, grid, dim3(32), 0, s, nullptr, 0, cfg, a);
-        case SPIN_DTYPE_BF16:
-            return launch_pdl(kv_attend_kernel<__nv_bfloat16>, grid, dim3(32), 0, s, nullptr, 0, cfg, a);
-        default: return launch_pdl(kv_attend_kernel<__half>, grid, dim3(32), 0, s, nullptr, 0, cfg, a);
+        case SPIN_DTYPE_F32: return launch_typed<float>(cfg, a, s);
+        case SPIN_DTYPE_BF16: return launch_typed<__nv_bfloat16>(cfg, a, s);
+        default: return launch_typed<__half>(cfg, a, s);
     }
 }
 

@@ -25,7 +25,7 @@ pytestmark = pytest.mark.gpu
 
 
 def check(dtype, heads, kvh, d, lens, rows=1, top_k=0, seed=0, spread=0.3, scale=None, n_slots=None, listed=None,
-          mutate=None, status_bits=0, q_size=1.0):
+          mutate=None, status_bits=0, q_size=1.0, max_slots=None):
     """One call against the oracle; `lens` are the requests' cached slots."""
     rng = np.random.default_rng(seed)
     R = len(lens)
@@ -44,7 +44,9 @@ def check(dtype, heads, kvh, d, lens, rows=1, top_k=0, seed=0, spread=0.3, scale
                 listed[b, r, :m] = np.sort(rng.permutation(int(n_slots[b, r]))[:m])
     if mutate:
         mutate(rng, pools, table, n_slots, listed)
-    cfg = spin.make_kv_config(R, max(max(lens), 1), rows, heads, kvh, d, dtype, scale)
+    if max_slots:
+        table = np.pad(table, ((0, 0), (0, -(-max_slots // 64) - table.shape[1])), constant_values=-1)
+    cfg = spin.make_kv_config(R, max_slots or max(max(lens), 1), rows, heads, kvh, d, dtype, scale)
     dv = [_kv.dev(x) for x in pools]
     before = [x.clone() for x in dv]
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -112,6 +114,14 @@ def test_many_requests_of_mixed_length(dtype):
     lens = np.exp(rng.uniform(0, np.log(3000), 70)).astype(int)
     lens[::9] = 0
     check(dtype, 8, 2, 64, list(lens), seed=6)
+
+
+@pytest.mark.parametrize("lens", [[1], [70], [2000, 100, 0, 7], [0, 0, 0], [64] * 9, [130, 0, 0, 0, 4000]])
+def test_short_requests_under_a_large_capacity(lens):
+    """The launch is sized by max_slots: most of its CTAs find no work."""
+    check("bf16", 16, 2, 128, lens, max_slots=100000, seed=len(lens))
+    check("f32", 4, 4, 64, lens, max_slots=100000, top_k=900, seed=len(lens))
+    check("bf16", 64, 1, 128, lens, max_slots=100000, rows=3, seed=len(lens))
 
 
 def test_long_context():
