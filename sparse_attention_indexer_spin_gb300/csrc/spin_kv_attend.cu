@@ -52,6 +52,11 @@ __device__ __forceinline__ float lg2(float x) {
     return y;
 }
 
+// Value scales that their logarithm stands for: positive and neither tiny nor huge.  The others
+// count as 2^-100 .. 2^100 in the reference, times a ratio.
+__device__ __forceinline__ bool in_log_range(float v) { return v >= 7.888609e-31f && v <= 1.2676506e30f; }
+__device__ __forceinline__ float scale_log2(float v) { return fminf(fmaxf(lg2(fabsf(v)), -100.0f), 100.0f); }
+
 // Four e4m3 codes as two pairs of f16 (exact).
 __device__ __forceinline__ void codes_to_f16(uint32_t c, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
@@ -127,18 +132,27 @@ template <int D> __device__ __forceinline__ uint32_t value_at(int row, int x) {
     else return (uint32_t)(row * D + (x >> 3) * 128 + (((x & 7) ^ (row & 6)) << 4));
 }
 
-template <int D> struct AtStage {  // byte offsets in a stage
-    static constexpr int kValues = kAtTile * D, kKs = 2 * kAtTile * D, kVs = kKs + 4 * kAtTile, kMask = kVs + 4 * kAtTile;
-    static constexpr int kBytes = kMask + 128;
+// Rows 32 / (D / 16) apart keep their place in a line of keys; the value swizzle flips these bits.
+template <int D> __device__ __forceinline__ constexpr uint32_t value_flip(int i) {
+    return D == 128 ? (uint32_t)(i & 1) << 6 : D == 256 ? (uint32_t)(i & 3) << 5 : 0u;
+}
+
+template <int D, bool SPARSE> struct AtStage {  // byte offsets in a stage
+    // codes of keys and values, then words.  With a list: per slot the key scale, value scale, log2
+    // of the value scale, its reciprocal (before those are known: the mask of live slots, at kMask).
+    // Without: key scale, value scale and mask of the tile's page.
+    static constexpr int kValues = kAtTile * D, kKs = 2 * kAtTile * D, kVs = kKs + (SPARSE ? 128 : 4),
+                         kLv = kVs + 128, kIv = kLv + 128, kMask = SPARSE ? kIv : kVs + 4;
+    static constexpr int kBytes = kKs + (SPARSE ? 512 : 128);
 };
 
-template <int D, int MT, bool SPLIT> struct AtSmem {
+template <int D, int MT, bool SPLIT, bool SPARSE> struct AtSmem {
     static constexpr int kRows = 16 * MT;
-    static constexpr int kRing = kAtWarps * kAtStages * AtStage<D>::kBytes;
+    static constexpr int kRing = kAtWarps * kAtStages * AtStage<D, SPARSE>::kBytes;
     static constexpr int kMerge = kAtWarps * kRows * D * 4;          // shares the ring's memory
     static constexpr int kMain = kRing > kMerge ? kRing : kMerge;
     static constexpr int kQ = MT * (SPLIT ? 2 : 1) * (D / 16) * 512;  // query fragments
-    static constexpr int kBytes = kMain + kQ + kRows * 8 + 2 * kAtWarps * kRows * 4 + kAtThreads * 8 + 64;
+    static constexpr int kBytes = kMain + kQ + kRows * 8 + 2 * kAtWarps * kRows * 4 + 128;
 };
 
 // Merged rows in shared memory: float4 f of a row is kept at f ^ rot, so that the eight lanes of
@@ -205,15 +219,18 @@ __device__ __forceinline__ int64_t cta_incl_scan64(int64_t v, int64_t* smem, int
     return s;
 }
 
+// CTAs on an SM: three where registers and shared memory allow
+template <int D, int MT, bool SPLIT> constexpr int at_ctas() { return D == 256 ? 1 : MT == 2 || (SPLIT && D == 128) ? 2 : 3; }
+
 // --------------------------------------------------------------------------- the kernel
 template <typename T, int D, int MT, bool SPARSE>
-__global__ void __launch_bounds__(kAtThreads, D == 256 ? 1 : 2)
+__global__ void __launch_bounds__(kAtThreads, at_ctas<D, MT, std::is_same<T, float>::value>())
 kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_constant__ KvAttendArgs a, AtPlan plan) {
     pdl_begin();
     constexpr bool SPLIT = std::is_same<T, float>::value;
     constexpr bool QREG = MT == 1 && !SPLIT && D <= 128;  // query fragments stay in registers
-    using L = AtSmem<D, MT, SPLIT>;
-    using St = AtStage<D>;
+    using L = AtSmem<D, MT, SPLIT, SPARSE>;
+    using St = AtStage<D, SPARSE>;
     constexpr int NT = D / 8;       // column tiles of o
     constexpr int KS = D / 16;      // contraction steps of q . k
     extern __shared__ __align__(128) unsigned char smem[];
@@ -247,11 +264,12 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
     int v = 0;          // request the part begins in
     int64_t into = 0;   // units of that request before it
     if (plan.split) {
+        const bool one = plan.n_virtual <= kAtThreads;  // the first pass has every request's place
+        int64_t u = 0, inc = 0, sum;
         for (int base = 0; base < plan.n_virtual; base += kAtThreads) {
             const int x = base + tid;
-            const int64_t u = x < plan.n_virtual ? (virtual_len<SPARSE>(cfg, a, x) + kAtUnit - 1) / kAtUnit : 0;
-            int64_t sum;
-            cta_incl_scan64(u * per_request, sScan, &sum);
+            u = x < plan.n_virtual ? (virtual_len<SPARSE>(cfg, a, x) + kAtUnit - 1) / kAtUnit * per_request : 0;
+            inc = cta_incl_scan64(u, sScan, &sum);
             total += sum;
         }
         // every CTA that takes part has a unit at least: a divided job's pieces are those of
@@ -260,20 +278,18 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
         if (me < G) {
             begin = total * me / G;
             end = total * (me + 1) / G;
-        }
-        if (begin < end) {
             int64_t before = 0;
-            if (tid == 0) sScan[8] = -1;
             for (int base = 0; base < plan.n_virtual; base += kAtThreads) {
                 const int x = base + tid;
-                const int64_t u = x < plan.n_virtual ? (virtual_len<SPARSE>(cfg, a, x) + kAtUnit - 1) / kAtUnit : 0;
-                int64_t sum;
-                const int64_t inc = before + cta_incl_scan64(u * per_request, sScan, &sum);
-                if (inc > begin && inc - u * per_request <= begin) {
-                    sScan[8] = x;
-                    sScan[9] = inc - u * per_request;
+                if (!one) {
+                    u = x < plan.n_virtual ? (virtual_len<SPARSE>(cfg, a, x) + kAtUnit - 1) / kAtUnit * per_request : 0;
+                    inc = before + cta_incl_scan64(u, sScan, &sum);
+                    before += sum;
                 }
-                before += sum;
+                if (inc > begin && inc - u <= begin) {
+                    sScan[8] = x;
+                    sScan[9] = inc - u;
+                }
                 if (before > begin) break;
             }
             __syncthreads();
@@ -316,6 +332,90 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
         const int64_t b = SPARSE ? v / a.rows : v;
         const int64_t br0 = SPARSE ? v : (int64_t)v * a.rows;  // first (request, row)
         const int m0 = mc * L::kRows, mrows = min(L::kRows, M - m0);
+
+        // ---- this warp's tiles: tile0 + wid, + kAtWarps, ... below tile1
+        const int tile0 = u0 * (kAtUnit / kAtTile), tile1 = min(u1 * (kAtUnit / kAtTile), (len + kAtTile - 1) / kAtTile);
+        const int nt = max(0, (tile1 - tile0 - wid + kAtWarps - 1) / kAtWarps);
+        const uint32_t ring = smem_u32(smem) + (uint32_t)(wid * kAtStages * St::kBytes);
+        const int32_t* table = a.block_table + b * a.bt_stride;
+        const int row_n = SPARSE ? row_slots(a, br0, cfg.max_slots) : 0;
+        const int64_t row_bytes = (int64_t)kvh * d;
+
+        // Entries and pages are read ahead of the copies that need them: a list entry two tiles, a
+        // page one tile.
+        auto entry = [&](int k) -> int {  // slot of this lane in the warp's k-th tile, -1: none
+            const int t = tile0 + wid + k * kAtWarps;
+            if constexpr (SPARSE) {
+                const int e = t * kAtTile + lane;
+                if (k >= nt || e >= a.top_k) return -1;
+                const int i = a.list[(int64_t)v * a.top_k + e];
+                if (i >= 0 && i < row_n) return i;
+                if (i != -1) set_status(a.status, SPIN_STATUS_BAD_LIST);
+                return -1;
+            } else {
+                const int i = t * kAtTile + lane;
+                return k < nt && i < len ? i : -1;
+            }
+        };
+        auto page_at = [&](int i) -> int {
+            if (i < 0) return -1;
+            const int p = table[i >> 6];
+            if (p >= 0 && p < a.n_pages) return p;
+            set_status(a.status, SPIN_STATUS_BAD_PAGE);
+            return -1;
+        };
+        int e_now = entry(0), e_next = entry(1), p_now = page_at(e_now);
+
+        constexpr int CH = D / 16;             // 16-byte chunks of a row
+        constexpr int RS = 32 / CH;            // rows a warp copies at a time
+        const int crow = lane / CH, cx = lane % CH;
+        const uint32_t kdst = ring + key_at<D>(crow, cx), vdst = ring + St::kValues + value_at<D>(crow, cx);
+        const bool in_row = 16 * cx < d;
+        const int64_t lane_src = (SPARSE ? 0 : crow * row_bytes) + (int64_t)g * d + 16 * cx;
+        auto issue = [&](int k) {  // the k-th tile's copies into its stage
+            if (k < nt) {
+                const uint32_t so = (uint32_t)((k % kAtStages) * St::kBytes);
+                const bool live = p_now >= 0;
+                const uint32_t mask = __ballot_sync(0xffffffffu, live);
+                if constexpr (SPARSE) {
+                    const int64_t row = live ? (int64_t)p_now * kBlock + (e_now & 63) : 0;
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) {
+                        const int from = crow + RS * i;
+                        const int64_t src = __shfl_sync(0xffffffffu, row, from) * row_bytes + lane_src;
+                        const bool ok = ((mask >> from) & 1u) && in_row;
+                        cp16(kdst + so + 512 * i, a.k_pool + (ok ? src : 0), ok);
+                        cp16((vdst ^ value_flip<D>(i)) + so + 512 * i, a.v_pool + (ok ? src : 0), ok);
+                    }
+                    const int64_t sc = live ? (int64_t)p_now * kvh + g : 0;
+                    cp4(ring + so + St::kKs + 4 * lane, a.k_scale + sc, live);
+                    cp4(ring + so + St::kVs + 4 * lane, a.v_scale + sc, live);
+                } else {
+                    // one page: the live slots are the first ones
+                    const int n_live = __popc(mask), page = __shfl_sync(0xffffffffu, p_now, 0);
+                    const int first = (tile0 + wid + k * kAtWarps) * kAtTile & (kBlock - 1);
+                    const int64_t src = n_live ? ((int64_t)page * kBlock + first) * row_bytes + lane_src : 0;
+                    const int64_t step = RS * row_bytes;
+#pragma unroll
+                    for (int i = 0; i < CH; ++i) {
+                        const bool ok = crow + RS * i < n_live && in_row;
+                        cp16(kdst + so + 512 * i, a.k_pool + (ok ? src + i * step : 0), ok);
+                        cp16((vdst ^ value_flip<D>(i)) + so + 512 * i, a.v_pool + (ok ? src + i * step : 0), ok);
+                    }
+                    if (lane < 2)
+                        cp4(ring + so + (lane ? St::kVs : St::kKs), (lane ? a.v_scale : a.k_scale) + (n_live ? (int64_t)page * kvh + g : 0),
+                            n_live > 0);
+                }
+                if (lane == 0)
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(ring + so + St::kMask), "r"(mask) : "memory");
+                e_now = e_next;
+                p_now = page_at(e_now);
+                e_next = entry(k + 2);
+            }
+            cp_commit();
+        };
+#pragma unroll
+        for (int k = 0; k < kAtStages; ++k) issue(k);
 
         // ---- queries: row m is (row m / group, head g * group + m % group), scaled by a power
         // of two and rounded to f16, laid out as the fragments read them
@@ -383,67 +483,6 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
             for (int n = 0; n < NT; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.0f;
         }
 
-        // ---- this warp's tiles: tile0 + wid, + kAtWarps, ... below tile1
-        const int tile0 = u0 * (kAtUnit / kAtTile), tile1 = min(u1 * (kAtUnit / kAtTile), (len + kAtTile - 1) / kAtTile);
-        const int nt = max(0, (tile1 - tile0 - wid + kAtWarps - 1) / kAtWarps);
-        const uint32_t ring = smem_u32(smem) + (uint32_t)(wid * kAtStages * St::kBytes);
-        const int32_t* table = a.block_table + b * a.bt_stride;
-        const int row_n = SPARSE ? row_slots(a, br0, cfg.max_slots) : 0;
-        const int64_t row_bytes = (int64_t)kvh * d;
-
-        // Entries and pages are read ahead of the copies that need them: a list entry two tiles, a
-        // page one tile.
-        auto entry = [&](int k) -> int {  // slot of this lane in the warp's k-th tile, -1: none
-            const int t = tile0 + wid + k * kAtWarps;
-            if constexpr (SPARSE) {
-                const int e = t * kAtTile + lane;
-                if (k >= nt || e >= a.top_k) return -1;
-                const int i = a.list[(int64_t)v * a.top_k + e];
-                if (i >= 0 && i < row_n) return i;
-                if (i != -1) set_status(a.status, SPIN_STATUS_BAD_LIST);
-                return -1;
-            } else {
-                const int i = t * kAtTile + lane;
-                return k < nt && i < len ? i : -1;
-            }
-        };
-        auto page_at = [&](int i) -> int {
-            if (i < 0) return -1;
-            const int p = table[i >> 6];
-            if (p >= 0 && p < a.n_pages) return p;
-            set_status(a.status, SPIN_STATUS_BAD_PAGE);
-            return -1;
-        };
-        int e_now = entry(0), e_next = entry(1), p_now = page_at(e_now);
-
-        auto issue = [&](int k) {  // the k-th tile's copies into its stage
-            if (k < nt) {
-                const uint32_t st = ring + (uint32_t)((k % kAtStages) * St::kBytes);
-                const bool live = p_now >= 0;
-                const int64_t off = live ? ((int64_t)p_now * kBlock + (e_now & 63)) * row_bytes + (int64_t)g * d : 0;
-                const int64_t so = live ? (int64_t)p_now * kvh + g : 0;
-                constexpr int CH = D / 16;  // chunks of a row
-#pragma unroll
-                for (int i = 0; i < CH; ++i) {
-                    const int row = (lane + 32 * i) / CH, x = lane % CH;
-                    const int64_t ro = __shfl_sync(0xffffffffu, off, row) + 16 * x;
-                    const bool ok = __shfl_sync(0xffffffffu, (int)live, row) && 16 * x < d;
-                    cp16(st + key_at<D>(row, x), a.k_pool + (ok ? ro : 0), ok);
-                    cp16(st + St::kValues + value_at<D>(row, x), a.v_pool + (ok ? ro : 0), ok);
-                }
-                cp4(st + St::kKs + 4 * lane, a.k_scale + so, live);
-                cp4(st + St::kVs + 4 * lane, a.v_scale + so, live);
-                const uint32_t mask = __ballot_sync(0xffffffffu, live);
-                if (lane == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + St::kMask), "r"(mask) : "memory");
-                e_now = e_next;
-                p_now = page_at(e_now);
-                e_next = entry(k + 2);
-            }
-            cp_commit();
-        };
-#pragma unroll
-        for (int k = 0; k < kAtStages; ++k) issue(k);
-
         for (int k = 0; k < nt; ++k) {
             cp_wait<kAtStages - 1>();
             __syncwarp();
@@ -488,36 +527,84 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
                 }
             }
 
-            // ---- weights
-            float ks[8], vs[8], lv[8];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint2 x = lds64(st + St::kKs + 4 * (8 * j + 2 * t4)), y = lds64(st + St::kVs + 4 * (8 * j + 2 * t4));
-                ks[2 * j] = __uint_as_float(x.x);
-                ks[2 * j + 1] = __uint_as_float(x.y);
-                vs[2 * j] = __uint_as_float(y.x);
-                vs[2 * j + 1] = __uint_as_float(y.y);
-                lv[2 * j] = fmaxf(lg2(fabsf(vs[2 * j])), -100.0f);
-                lv[2 * j + 1] = fmaxf(lg2(fabsf(vs[2 * j + 1])), -100.0f);
-            }
+            // ---- weights: 2^(t - m) vs, where t = qs ks s; with x = t + log2 vs they are 2^(x - m)
+            // and l gains them divided by vs
             const bool border = mask != 0xffffffffu || slot0 + kAtTile > nmin;
-            float top[MT][2];
+            float top[MT][2], lv[SPARSE ? 8 : 1], iv[SPARSE ? 8 : 1], c[MT][2];
+            bool odd = false;  // a value scale whose logarithm does not stand for it
+            if constexpr (SPARSE) {
+                uint32_t u;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(st + St::kVs + 4 * lane) : "memory");
+                const float v_ = __uint_as_float(u);
+                const bool fine = in_log_range(v_) || !((mask >> lane) & 1u);
+                odd = __any_sync(0xffffffffu, !fine);
+                const float lg = scale_log2(v_);
+                __syncwarp();  // every lane has read the mask
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(st + St::kLv + 4 * lane), "f"(lg) : "memory");
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(st + St::kIv + 4 * lane), "f"(in_log_range(v_) ? __frcp_rn(v_) : ex2(-lg)) : "memory");
+                __syncwarp();
+                float ks[8];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                top[i][0] = top[i][1] = ninf;
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t o4 = 4 * (8 * j + 2 * t4);
+                    const uint2 x = lds64(st + St::kKs + o4), y = lds64(st + St::kLv + o4), z = lds64(st + St::kIv + o4);
+                    ks[2 * j] = __uint_as_float(x.x), ks[2 * j + 1] = __uint_as_float(x.y);
+                    lv[2 * j] = __uint_as_float(y.x), lv[2 * j + 1] = __uint_as_float(y.y);
+                    iv[2 * j] = __uint_as_float(z.x), iv[2 * j + 1] = __uint_as_float(z.y);
+                }
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int i = 0; i < MT; ++i) {
+                    top[i][0] = top[i][1] = ninf;
+                    c[i][0] = c[i][1] = 1.0f;
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const int col = 2 * j + (x & 1), r = x >> 1;
-                        float y = s[i][j][x] * qs[i][r] * ks[col];
-                        if (border) {
-                            const int at_slot = 8 * j + 2 * t4 + (x & 1);
-                            if (!((mask >> at_slot) & 1u) || slot0 + at_slot >= nlim[i][r]) y = ninf;
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int col = 2 * j + (x & 1), r = x >> 1;
+                            float y = fmaf(s[i][j][x] * ks[col], qs[i][r], lv[col]);
+                            if (border && !((mask >> (8 * j + 2 * t4 + (x & 1))) & 1u)) y = ninf;
+                            s[i][j][x] = y;
+                            top[i][r] = fmaxf(top[i][r], y);
                         }
-                        s[i][j][x] = y;
-                        top[i][r] = fmaxf(top[i][r], y + lv[col]);
-                    }
+                }
+            } else {
+                uint32_t u, w;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(u) : "r"(st + St::kKs) : "memory");
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(st + St::kVs) : "memory");
+                const float ks = __uint_as_float(u), v_ = __uint_as_float(w);
+                odd = !in_log_range(v_);
+                lv[0] = scale_log2(v_);
+                iv[0] = odd ? ex2(-lv[0]) : __frcp_rn(v_);
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) c[i][r] = qs[i][r] * ks;
+                if (border) {
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                                for (int x = 2 * r; x < 2 * r + 2; ++x) {
+                                    const int at_slot = 8 * j + 2 * t4 + (x & 1);
+                                    const bool ok = ((mask >> at_slot) & 1u) && slot0 + at_slot < nlim[i][r];
+                                    s[i][j][x] = ok ? s[i][j][x] * c[i][r] : ninf;
+                                }
+                            c[i][r] = 1.0f;
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    top[i][0] = top[i][1] = ninf;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) top[i][x >> 1] = fmaxf(top[i][x >> 1], s[i][j][x] * c[i][x >> 1]);
+                    top[i][0] += lv[0];
+                    top[i][1] += lv[0];
+                }
             }
             bool move = false;
 #pragma unroll
@@ -547,23 +634,49 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
             uint4 pw[MT][SPLIT ? 2 : 1][2];
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
-                const float ref0 = mx[i][0] == ninf ? 0.0f : mx[i][0], ref1 = mx[i][1] == ninf ? 0.0f : mx[i][1];
-                uint32_t ph[8], pl[8];
+                float bias[2], add[2] = {0.0f, 0.0f};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float p[4];
+                for (int r = 0; r < 2; ++r) bias[r] = (SPARSE ? 0.0f : lv[0]) - (mx[i][r] == ninf ? 0.0f : mx[i][r]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        p[x] = ex2(s[i][j][x] - ((x >> 1) ? ref1 : ref0));
-                        lsum[i][x >> 1] += p[x];
-                        p[x] *= vs[2 * j + (x & 1)];
+                        const int r = x >> 1;
+                        const float p = ex2(SPARSE ? s[i][j][x] + bias[r] : fmaf(s[i][j][x], c[i][r], bias[r]));
+                        s[i][j][x] = p;
+                        add[r] = SPARSE ? fmaf(p, iv[SPARSE ? 2 * j + (x & 1) : 0], add[r]) : add[r] + p;
                     }
-                    ph[2 * j] = pack_f16(p[0], p[1]);
-                    ph[2 * j + 1] = pack_f16(p[2], p[3]);
+#pragma unroll
+                for (int r = 0; r < 2; ++r) lsum[i][r] = SPARSE ? lsum[i][r] + add[r] : fmaf(add[r], iv[0], lsum[i][r]);
+            }
+            if (odd) {  // zero, negative, tiny, huge or NaN: the ratio of scale and power of two
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t u;
+                        asm volatile("ld.shared.u32 %0, [%1];"
+                                     : "=r"(u)
+                                     : "r"(st + St::kVs + (SPARSE ? 4 * (8 * j + 2 * t4 + x) : 0))
+                                     : "memory");
+                        const float v_ = __uint_as_float(u), f = in_log_range(v_) ? 1.0f : v_ * ex2(-scale_log2(v_));
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) {
+                            s[i][j][x] *= f;
+                            s[i][j][2 + x] *= f;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                uint32_t ph[8], pl[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float p0 = s[i][j >> 1][2 * (j & 1)], p1 = s[i][j >> 1][2 * (j & 1) + 1];
+                    ph[j] = pack_f16(p0, p1);
                     if constexpr (SPLIT) {
-                        const float2 h0 = unpack_f16(ph[2 * j]), h1 = unpack_f16(ph[2 * j + 1]);
-                        pl[2 * j] = pack_f16(p[0] - h0.x, p[1] - h0.y);
-                        pl[2 * j + 1] = pack_f16(p[2] - h1.x, p[3] - h1.y);
+                        const float2 h = unpack_f16(ph[j]);
+                        pl[j] = pack_f16(p0 - h.x, p1 - h.y);
                     }
                 }
                 pw[i][0][0] = make_uint4(ph[0], ph[1], ph[2], ph[3]);
@@ -807,21 +920,23 @@ __global__ void __launch_bounds__(256) kv_attend_join_kernel(spin_kv_config cfg,
 }
 
 // ------------------------------------------------------------------------------ host side
+constexpr int kAtMostCtas = 3;
 static int at_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 // one row tile (16 query rows of a key/value head) a warp, two where there are more; a 256-wide
 // output leaves registers for one
 static int at_mtiles(int D, int M) { return M > 16 && D <= 128 ? 2 : 1; }
 
-// At least two CTAs' worth of records for any split launch.
+// Two records for every CTA of any variant.
 size_t kv_attend_workspace_bytes(const spin_kv_config& cfg, int, int) {
     const int D = at_dim(cfg.head_dim);
-    const size_t G = 2 * (size_t)device_sm_count();
+    const size_t G = kAtMostCtas * (size_t)device_sm_count();
     return (G * sizeof(int4) + 255) / 256 * 256 + G * 2 * 32 * (size_t)(D + 2) * sizeof(float);
 }
 
 template <typename T, int D, int MT, bool SPARSE>
 static cudaError_t launch_at(const spin_kv_config& cfg, const KvAttendArgs& a, cudaStream_t s) {
-    using L = AtSmem<D, MT, std::is_same<T, float>::value>;
+    constexpr bool SPLIT = std::is_same<T, float>::value;
+    using L = AtSmem<D, MT, SPLIT, SPARSE>;
     auto k = kv_attend_kernel<T, D, MT, SPARSE>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
     if (e != cudaSuccess) return e;
@@ -831,13 +946,13 @@ static cudaError_t launch_at(const spin_kv_config& cfg, const KvAttendArgs& a, c
     p.n_virtual = SPARSE ? cfg.n_req * a.rows : cfg.n_req;
     const int64_t jobs = (int64_t)p.n_virtual * cfg.kv_heads * p.mchunks;
     const int64_t most = ((SPARSE ? a.top_k : cfg.max_slots) + kAtUnit - 1) / kAtUnit;
-    const int64_t ctas = (D == 256 ? 1 : 2) * (int64_t)device_sm_count();
+    const int64_t ctas = at_ctas<D, MT, SPLIT>() * (int64_t)device_sm_count();
     // whole jobs: ceil(jobs / ctas) * most units on the busiest CTA; split: jobs * most / ctas
     p.split = (jobs + ctas - 1) / ctas * most > jobs * most / ctas + kAtSplitGain;
     const int64_t work = p.split ? jobs * ((most + kAtMinUnits - 1) / kAtMinUnits) : jobs;
     const int G = (int)(work < ctas ? work : ctas);
     p.owner = reinterpret_cast<int4*>(a.workspace);
-    p.rec = a.workspace + ((size_t)2 * device_sm_count() * sizeof(int4) + 255) / 256 * 64;
+    p.rec = a.workspace + ((size_t)kAtMostCtas * device_sm_count() * sizeof(int4) + 255) / 256 * 64;
     e = launch_pdl(k, dim3(G), dim3(kAtThreads), L::kBytes, s, nullptr, 0, cfg, a, p);
     if (e != cudaSuccess || !p.split) return e;
     return launch_pdl(kv_attend_join_kernel<T, D, MT>, dim3(G), dim3(256), 0, s, nullptr, 0, cfg, a, p,
