@@ -209,6 +209,12 @@ __device__ __forceinline__ void pdl_begin() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// The two halves for kernels that fill the SMs: pdl_wait() first, and pdl_trigger() only when a
+// CTA is nearly done, so that the next kernel's waiting CTAs do not hold slots that this grid or
+// its predecessor still needs (attention with its join launch: 76 us with pdl_begin(), 59 us so).
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Host side: launch `k` with programmatic stream serialization allowed, plus any extra
 // launch attributes (a cluster shape).
 template <typename... P, typename... A>

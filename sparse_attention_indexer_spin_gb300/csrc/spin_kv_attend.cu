@@ -28,12 +28,19 @@ namespace spin {
 
 constexpr int kAtWarps = 4;      // warps of a CTA: each takes every fourth tile of a segment
 constexpr int kAtThreads = 32 * kAtWarps;
+constexpr int kAtMostCtas = 3;   // CTAs on an SM
+constexpr int kAtMostSms = 512;  // bounds the pieces of a job
+constexpr int kAtMostPieces = kAtMostCtas * kAtMostSms;
 constexpr int kAtTile = 32;      // slots a warp works on at a time
 constexpr int kAtStages = 2;     // tiles in a warp's ring
 constexpr float kAtTop = 12.0f;  // log2 of the largest weight when the reference is set
 constexpr float kAtSlack = 3.0f; // a maximum may exceed that by this much before the reference moves
 constexpr int kAtUnit = 64;      // slots in a unit of work
-constexpr int kAtMinUnits = 2;   // units a CTA takes at least: a tile for each of its warps
+constexpr int kAtMinCost = 4;    // units a CTA takes at least
+// Starting a job costs about as much as this many units (its queries, its first pages and tiles,
+// the merge of its warps: 4 us beside 1.1 us a unit with the GPU full), and counts as such when the
+// work is divided.
+constexpr int kAtJobUnits = 4;
 // A job (request or request row, key/value head, chunk of query rows) is split over CTAs
 // unless whole jobs cost at most this many units more on the busiest CTA; the combining
 // launch costs about as much.
@@ -163,12 +170,19 @@ template <int D> __device__ __forceinline__ int merge_at(int row, int f) {
 }
 
 // ------------------------------------------------------------------------- work division
+// A job is a (request, or with a list request row; key/value head; chunk of query rows).  Its cost
+// is kAtJobUnits and then its units of slots.  A split launch lays the requests' costs end to end
+// and divides them evenly into ranks; `per` CTAs, one for each head and chunk, share a rank, so
+// that a page's heads, which lie side by side, are read at about the same time.
 struct AtPlan {
-    int split;      // jobs may be divided over CTAs
+    int split;      // jobs may be divided over ranks; else CTAs take whole jobs
     int mchunks;    // chunks of query rows per key/value head
+    int per;        // jobs of a request: kv_heads * mchunks
     int n_virtual;  // requests, or with lists request rows
+    int by_job;     // `owner` has an entry per job, else one per CTA
     float* rec;     // partial results: two records per CTA
-    int4* owner;    // per CTA: job it begins and does not finish, and the number of pieces
+    int4* owner;    // a divided job (request, job of the request), its first rank and number of pieces (by_job:
+                    // of this job; else: of the job that this CTA begins and does not finish); w = 0: none
 };
 
 // Slots of request b's longest row (its own row's with a list); bad lengths count as 0.
@@ -226,7 +240,7 @@ template <int D, int MT, bool SPLIT> constexpr int at_ctas() { return D == 256 ?
 template <typename T, int D, int MT, bool SPARSE>
 __global__ void __launch_bounds__(kAtThreads, at_ctas<D, MT, std::is_same<T, float>::value>())
 kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_constant__ KvAttendArgs a, AtPlan plan) {
-    pdl_begin();
+    pdl_wait();
     constexpr bool SPLIT = std::is_same<T, float>::value;
     constexpr bool QREG = MT == 1 && !SPLIT && D <= 128;  // query fragments stay in registers
     using L = AtSmem<D, MT, SPLIT, SPARSE>;
@@ -243,86 +257,89 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
     const int H = cfg.n_heads, kvh = cfg.kv_heads, d = cfg.head_dim, group = H / kvh;
     const int rows = SPARSE ? 1 : a.rows, M = group * rows;
-    const int me = blockIdx.x;
-    int64_t G = gridDim.x;  // CTAs with work, once the work is known
-    const int64_t per_request = (int64_t)kvh * plan.mchunks;
+    const int me = blockIdx.x, mine_of = me % plan.per, rank = me / plan.per;
     const float ninf = __uint_as_float(0xff800000u);
 
-    // requests without any slot: zeros
-    for (int v = me; v < plan.n_virtual; v += gridDim.x) {
-        if (virtual_len<SPARSE>(cfg, a, v) > 0) continue;
-        const int64_t base = (int64_t)v * rows * H;
-        for (int64_t e = tid; e < (int64_t)rows * H * d / 4; e += kAtThreads)
-            store4(reinterpret_cast<T*>(a.out) + base * d + 4 * e, make_float4(0, 0, 0, 0));
-        if (a.lse)
-            for (int e = tid; e < rows * H; e += kAtThreads) a.lse[base + e] = ninf;
-    }
-
-    // this CTA's part of the work: units [begin, end) of all jobs laid end to end (split), or
-    // jobs me, me + G, ... whole
-    int64_t total = 0, begin = 0, end = 0;
-    int v = 0;          // request the part begins in
-    int64_t into = 0;   // units of that request before it
+    // this CTA's part of the work: [begin, end) of all requests' cost (split), or jobs me,
+    // me + gridDim.x, ... whole
+    int64_t total = 0, begin = 0, end = 0, ranks = gridDim.x / plan.per;
+    int v = 0;             // request the part begins in
+    int64_t into = 0;      // cost of that request before it
+    int len_v = -1;        // that request's slots, -1: not known yet
+    auto cost = [&](int len) -> int64_t { return len ? (len + kAtUnit - 1) / kAtUnit + kAtJobUnits : 0; };
     if (plan.split) {
         const bool one = plan.n_virtual <= kAtThreads;  // the first pass has every request's place
-        int64_t u = 0, inc = 0, sum;
+        int len = 0;
+        int64_t inc = 0, sum;
         for (int base = 0; base < plan.n_virtual; base += kAtThreads) {
             const int x = base + tid;
-            u = x < plan.n_virtual ? (virtual_len<SPARSE>(cfg, a, x) + kAtUnit - 1) / kAtUnit * per_request : 0;
-            inc = cta_incl_scan64(u, sScan, &sum);
+            len = x < plan.n_virtual ? virtual_len<SPARSE>(cfg, a, x) : 0;
+            inc = cta_incl_scan64(cost(len), sScan, &sum);
             total += sum;
         }
-        // every CTA that takes part has a unit at least: a divided job's pieces are those of
-        // consecutive CTAs
-        G = min(G, (total + kAtMinUnits - 1) / kAtMinUnits);
-        if (me < G) {
-            begin = total * me / G;
-            end = total * (me + 1) / G;
+        // every rank that takes part has some cost at least: a divided job's pieces are those of
+        // consecutive ranks
+        ranks = min(ranks, (total + kAtMinCost - 1) / kAtMinCost);
+        if (rank < ranks) {
+            begin = total * rank / ranks;
+            end = total * (rank + 1) / ranks;
             int64_t before = 0;
             for (int base = 0; base < plan.n_virtual; base += kAtThreads) {
                 const int x = base + tid;
                 if (!one) {
-                    u = x < plan.n_virtual ? (virtual_len<SPARSE>(cfg, a, x) + kAtUnit - 1) / kAtUnit * per_request : 0;
-                    inc = before + cta_incl_scan64(u, sScan, &sum);
+                    len = x < plan.n_virtual ? virtual_len<SPARSE>(cfg, a, x) : 0;
+                    inc = before + cta_incl_scan64(cost(len), sScan, &sum);
                     before += sum;
                 }
-                if (inc > begin && inc - u <= begin) {
+                if (inc > begin && inc - cost(len) <= begin) {
                     sScan[8] = x;
-                    sScan[9] = inc - u;
+                    sScan[9] = begin - (inc - cost(len));
+                    sScan[10] = len;
                 }
                 if (before > begin) break;
             }
             __syncthreads();
             v = (int)sScan[8];
-            into = begin - sScan[9];
+            into = sScan[9];
+            len_v = (int)sScan[10];
         }
-        if (tid == 0) plan.owner[me] = make_int4(-1, 0, 0, 0);
+        if (tid == 0 && !plan.by_job) plan.owner[me].w = 0;
     }
 
     int64_t job = me;   // whole jobs
     for (int64_t at = begin;;) {
         // ---- the next segment: job (v, g, mc), units [u0, u1) of its `units`
         int g, mc, len, units, u0, u1;
+        int64_t span = 0, first = 0, mine = 0;  // the job's cost, where this CTA enters it, how much it takes
         if (plan.split) {
             if (at >= end) break;
             for (;;) {
-                len = virtual_len<SPARSE>(cfg, a, v);
-                units = (len + kAtUnit - 1) / kAtUnit;
-                if (into < units * per_request) break;
+                if (len_v < 0) len_v = virtual_len<SPARSE>(cfg, a, v);
+                if (into < cost(len_v)) break;
                 into = 0;
+                len_v = -1;
                 ++v;
             }
-            const int64_t j = into / units;
-            g = (int)(j / plan.mchunks);
-            mc = (int)(j % plan.mchunks);
-            u0 = (int)(into % units);
-            u1 = (int)min((int64_t)units, u0 + (end - at));
+            len = len_v;
+            units = (len + kAtUnit - 1) / kAtUnit;
+            span = units + kAtJobUnits;
+            g = mine_of / plan.mchunks;
+            mc = mine_of % plan.mchunks;
+            first = into;
+            mine = min(span - first, end - at);
+            u0 = (int)max((int64_t)0, first - kAtJobUnits);
+            u1 = (int)max((int64_t)0, first + mine - kAtJobUnits);
+            if (u0 == u1) {  // the part ends before the job's first unit
+                at += mine;
+                into += mine;
+                continue;
+            }
         } else {
-            if (job >= plan.n_virtual * per_request) break;
-            v = (int)(job / per_request);
-            g = (int)(job % per_request / plan.mchunks);
+            if (job >= (int64_t)plan.n_virtual * plan.per) break;
+            v = (int)(job / plan.per);
+            g = (int)(job % plan.per / plan.mchunks);
             mc = (int)(job % plan.mchunks);
-            job += G;
+            job += gridDim.x;
             len = virtual_len<SPARSE>(cfg, a, v);
             if (len == 0) continue;
             units = (len + kAtUnit - 1) / kAtUnit;
@@ -774,6 +791,7 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
             __syncwarp();
             issue(k + kAtStages);
         }
+        if (plan.split ? at + mine >= end : job >= (int64_t)plan.n_virtual * plan.per) pdl_trigger();
         cp_wait<0>();
         __syncthreads();   // the ring is free: the warps' results go there
 
@@ -844,83 +862,142 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
             }
         }
         if (plan.split) {
-            if (tid == 0 && u0 == 0 && u1 < units) {
-                // the CTA that holds the job's last unit
-                const int64_t last = at + units - 1;
-                int64_t c = last * G / total;
-                while (total * (c + 1) / G <= last) ++c;
-                while (total * c / G > last) --c;
-                plan.owner[me] = make_int4(v, g, mc, (int)(c - me) + 1);
+            if (tid == 0 && u0 == 0) {
+                int4 own = make_int4(v, mine_of, rank, 0);
+                if (u1 < units) {  // up to the rank that holds the end of the job's cost
+                    const int64_t last = at - first + span - 1;
+                    int64_t c = last * ranks / total;
+                    while (total * (c + 1) / ranks <= last) ++c;
+                    while (total * c / ranks > last) --c;
+                    own.w = (int)(c - rank) + 1;
+                }
+                if (plan.by_job) plan.owner[(int64_t)v * plan.per + mine_of] = own;
+                else if (own.w) plan.owner[me] = own;
             }
-            at += u1 - u0;
-            into += u1 - u0;
+            at += mine;
+            into += mine;
         }
         __syncthreads();
     }
-}
 
-// Joins the pieces of the jobs that were divided: the owner's second record, then the first
-// records of the CTAs after it.  One warp per query row.
-template <typename T, int D, int MT>
-__global__ void __launch_bounds__(256) kv_attend_join_kernel(spin_kv_config cfg, KvAttendArgs a, AtPlan plan, int rows) {
-    pdl_begin();
-    constexpr int ROWS = 16 * MT, REC = ROWS * (D + 2), F = D / 32;
-    const int4 job = plan.owner[blockIdx.x];
-    if (job.x < 0) return;
-    const int lane = threadIdx.x & 31, H = cfg.n_heads, d = cfg.head_dim, group = H / cfg.kv_heads;
-    const int m0 = job.z * ROWS, mrows = min(ROWS, group * rows - m0), pieces = job.w;
-    const float ninf = __uint_as_float(0xff800000u);
-    const float* rec0 = plan.rec + (int64_t)(2 * blockIdx.x + 1) * REC;
-    const float* rec1 = plan.rec + (int64_t)(2 * blockIdx.x + 2) * REC;  // piece p >= 1: rec1 + 2 (p - 1) REC
-    for (int m = threadIdx.x >> 5; m < mrows; m += 8) {
-        float top = ninf;
-        for (int p = lane; p < pieces; p += 32)
-            top = fmaxf(top, (p ? rec1 + (int64_t)2 * (p - 1) * REC : rec0)[ROWS * D + 2 * m]);
-#pragma unroll
-        for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-        float l = 0.0f, acc[F];
-#pragma unroll
-        for (int i = 0; i < F; ++i) acc[i] = 0.0f;
-#pragma unroll 8
-        for (int p = 0; p < pieces; ++p) {
-            const float* r = p ? rec1 + (int64_t)2 * (p - 1) * REC : rec0;
-            const float mw = r[ROWS * D + 2 * m];
-            const float c = mw == ninf ? 0.0f : ex2(mw - top);
-            l = fmaf(c, r[ROWS * D + 2 * m + 1], l);
-            float x[F];
-            if constexpr (F == 2) {
-                const float2 y = reinterpret_cast<const float2*>(r + m * D)[lane];
-                x[0] = y.x; x[1] = y.y;
-            } else {
-#pragma unroll
-                for (int i = 0; i < F; i += 4) {
-                    const float4 y = reinterpret_cast<const float4*>(r + m * D)[lane * (F / 4) + i / 4];
-                    x[i] = y.x; x[i + 1] = y.y; x[i + 2] = y.z; x[i + 3] = y.w;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < F; ++i) acc[i] = fmaf(c, x[i], acc[i]);
-        }
-        const int64_t v = job.x;
-        const int64_t bh = (v * rows + (m0 + m) / group) * H + (int64_t)job.y * group + (m0 + m) % group;
-        const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-        T* out = reinterpret_cast<T*>(a.out) + bh * d;
-#pragma unroll
-        for (int i = 0; i < F; ++i) {
-            const int c = lane * F + i;
-            const float y = l == 0.0f ? 0.0f : acc[i] * inv;
-            if (c < d) {
-                if constexpr (std::is_same<T, float>::value) out[c] = y;
-                else if constexpr (std::is_same<T, __half>::value) out[c] = __float2half_rn(y);
-                else out[c] = __float2bfloat16_rn(y);
-            }
-        }
-        if (a.lse && lane == 0) a.lse[bh] = l == 0.0f ? ninf : ((top == ninf ? 0.0f : top) + log2f(l)) * 0.6931471805599453f;
+    // requests without any slot: zeros
+    for (int x = me; x < plan.n_virtual; x += gridDim.x) {
+        if (virtual_len<SPARSE>(cfg, a, x) > 0) continue;
+        const int64_t base = (int64_t)x * rows * H;
+        for (int64_t e = tid; e < (int64_t)rows * H * d / 4; e += kAtThreads)
+            store4(reinterpret_cast<T*>(a.out) + base * d + 4 * e, make_float4(0, 0, 0, 0));
+        if (a.lse)
+            for (int e = tid; e < rows * H; e += kAtThreads) a.lse[base + e] = ninf;
+        if (plan.split && plan.by_job)
+            for (int e = tid; e < plan.per; e += kAtThreads) plan.owner[(int64_t)x * plan.per + e].w = 0;
     }
 }
 
+// Joins the pieces of the jobs that were divided: its first rank's second record, then the first
+// records of the ranks after it.  One CTA per job and query row: the pieces' factors first, then
+// each warp adds up every fourth piece.
+constexpr int kJoinWarps = 4;
+
+template <typename T, int D, int MT>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+kv_attend_join_kernel(spin_kv_config cfg, KvAttendArgs a, AtPlan plan, int rows) {
+    pdl_wait();
+    constexpr int ROWS = 16 * MT, REC = ROWS * (D + 2), F = D / 32;
+    __shared__ float s_c[kAtMostPieces], s_w[kAtMostPieces], s_top[kJoinWarps], s_l[kJoinWarps];
+    __shared__ __align__(16) float s_acc[kJoinWarps][D];
+    const int4 job = plan.owner[blockIdx.x];
+    if (job.w == 0) return;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, H = cfg.n_heads, d = cfg.head_dim;
+    const int group = H / cfg.kv_heads, g = job.y / plan.mchunks, m0 = job.y % plan.mchunks * ROWS, m = blockIdx.y;
+    const int pieces = job.w;
+    if (m >= min(ROWS, group * rows - m0)) return;
+    const float ninf = __uint_as_float(0xff800000u);
+    // CTA c has records 2c and 2c + 1; piece p lies in the first record of rank job.z + p, the first
+    // piece in the second of its rank
+    const float* rec = plan.rec + (int64_t)2 * (job.z * plan.per + job.y) * REC;
+    const int64_t step = (int64_t)2 * plan.per * REC;
+    auto at = [&](int p) -> const float* { return rec + (p ? p * step : REC); };
+    // a warp's first pieces are on their way while the factors are found
+    constexpr int AHEAD = 16 / F;
+    float x[AHEAD][F];
+    auto load = [&](float (&to)[F], int p) {
+        const float* r = at(p) + m * D + lane * F;
+        if constexpr (F == 2) {
+            const float2 y = *reinterpret_cast<const float2*>(r);
+            to[0] = y.x; to[1] = y.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < F; i += 4) {
+                const float4 y = *reinterpret_cast<const float4*>(r + i);
+                to[i] = y.x; to[i + 1] = y.y; to[i + 2] = y.z; to[i + 3] = y.w;
+            }
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+        if (wid + k * kJoinWarps < pieces) load(x[k], wid + k * kJoinWarps);
+    float top = ninf, l = 0.0f;
+    for (int p = tid; p < pieces; p += 32 * kJoinWarps) {
+        const float2 ml = *reinterpret_cast<const float2*>(at(p) + ROWS * D + 2 * m);
+        s_c[p] = ml.x;
+        s_w[p] = ml.y;
+        top = fmaxf(top, ml.x);
+    }
+#pragma unroll
+    for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+    if (lane == 0) s_top[wid] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_top[w]);
+    for (int p = tid; p < pieces; p += 32 * kJoinWarps) {
+        const float c = s_c[p] == ninf ? 0.0f : ex2(s_c[p] - top);
+        s_c[p] = c;
+        l = fmaf(c, s_w[p], l);
+    }
+#pragma unroll
+    for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
+    if (lane == 0) s_l[wid] = l;
+    __syncthreads();
+    l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) l += s_l[w];
+    float acc[F];
+#pragma unroll
+    for (int i = 0; i < F; ++i) acc[i] = 0.0f;
+    for (int base = wid; base < pieces; base += AHEAD * kJoinWarps) {
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int p = base + k * kJoinWarps;
+            if (p >= pieces) break;
+            const float c = s_c[p];
+#pragma unroll
+            for (int i = 0; i < F; ++i) acc[i] = fmaf(c, x[k][i], acc[i]);
+        }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int p = base + (AHEAD + k) * kJoinWarps;
+            if (p < pieces) load(x[k], p);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < F; ++i) s_acc[wid][lane * F + i] = acc[i];
+    __syncthreads();
+    const int64_t bh = ((int64_t)job.x * rows + (m0 + m) / group) * H + (int64_t)g * group + (m0 + m) % group;
+    const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+    for (int f = tid; f < d / 4; f += 32 * kJoinWarps) {
+        float4 y = make_float4(0, 0, 0, 0);
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            const float4 x = *reinterpret_cast<const float4*>(&s_acc[w][4 * f]);
+            y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
+        }
+        if (l == 0.0f) y = make_float4(0, 0, 0, 0);
+        store4(reinterpret_cast<T*>(a.out) + bh * d + 4 * f, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+    }
+    if (a.lse && tid == 0) a.lse[bh] = l == 0.0f ? ninf : ((top == ninf ? 0.0f : top) + log2f(l)) * 0.6931471805599453f;
+}
+
 // ------------------------------------------------------------------------------ host side
-constexpr int kAtMostCtas = 3;
 static int at_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 // one row tile (16 query rows of a key/value head) a warp, two where there are more; a 256-wide
 // output leaves registers for one
@@ -944,19 +1021,21 @@ static cudaError_t launch_at(const spin_kv_config& cfg, const KvAttendArgs& a, c
     AtPlan p;
     p.mchunks = (M + L::kRows - 1) / L::kRows;
     p.n_virtual = SPARSE ? cfg.n_req * a.rows : cfg.n_req;
-    const int64_t jobs = (int64_t)p.n_virtual * cfg.kv_heads * p.mchunks;
+    p.per = cfg.kv_heads * p.mchunks;
+    const int64_t jobs = (int64_t)p.n_virtual * p.per;
     const int64_t most = ((SPARSE ? a.top_k : cfg.max_slots) + kAtUnit - 1) / kAtUnit;
-    const int64_t ctas = at_ctas<D, MT, SPLIT>() * (int64_t)device_sm_count();
+    const int64_t ctas = at_ctas<D, MT, SPLIT>() * (int64_t)(device_sm_count() < kAtMostSms ? device_sm_count() : kAtMostSms);
     // whole jobs: ceil(jobs / ctas) * most units on the busiest CTA; split: jobs * most / ctas
-    p.split = (jobs + ctas - 1) / ctas * most > jobs * most / ctas + kAtSplitGain;
-    const int64_t work = p.split ? jobs * ((most + kAtMinUnits - 1) / kAtMinUnits) : jobs;
-    const int G = (int)(work < ctas ? work : ctas);
+    const int64_t ranks = ctas / p.per, most_ranks = p.n_virtual * (most + kAtJobUnits + kAtMinCost - 1) / kAtMinCost;
+    p.split = ranks > 0 && (jobs + ctas - 1) / ctas * most > jobs * most / (ranks * p.per) + kAtSplitGain;
+    const int G = (int)(p.split ? (most_ranks < ranks ? most_ranks : ranks) * p.per : jobs < ctas ? jobs : ctas);
+    p.by_job = jobs <= G;
     p.owner = reinterpret_cast<int4*>(a.workspace);
     p.rec = a.workspace + ((size_t)kAtMostCtas * device_sm_count() * sizeof(int4) + 255) / 256 * 64;
     e = launch_pdl(k, dim3(G), dim3(kAtThreads), L::kBytes, s, nullptr, 0, cfg, a, p);
     if (e != cudaSuccess || !p.split) return e;
-    return launch_pdl(kv_attend_join_kernel<T, D, MT>, dim3(G), dim3(256), 0, s, nullptr, 0, cfg, a, p,
-                      SPARSE ? 1 : a.rows);
+    return launch_pdl(kv_attend_join_kernel<T, D, MT>, dim3(p.by_job ? (unsigned)jobs : G, M < L::kRows ? M : L::kRows),
+                      dim3(32 * kJoinWarps), 0, s, nullptr, 0, cfg, a, p, SPARSE ? 1 : a.rows);
 }
 
 template <typename T, int D, int MT>
