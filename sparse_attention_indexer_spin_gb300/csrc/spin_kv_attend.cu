@@ -16,71 +16,23 @@
 // value scale costs no precision, and weights lose bits only below 2^-26 of the largest.  The
 // reference moves only when a maximum exceeds it by more than 2^3, which spares most of the
 // rescaling of o.
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
-
-#include <type_traits>
-
-#include "spin_common.cuh"
-#include "spin_internal.h"
+#include "spin_kv_attend.cuh"
 
 namespace spin {
 
 constexpr int kAtWarps = 4;      // warps of a CTA: each takes every fourth tile of a segment
 constexpr int kAtThreads = 32 * kAtWarps;
-constexpr int kAtMostCtas = 3;   // CTAs on an SM
-constexpr int kAtMostSms = 512;  // bounds the pieces of a job
-constexpr int kAtMostPieces = kAtMostCtas * kAtMostSms;
 constexpr int kAtTile = 32;      // slots a warp works on at a time
 constexpr int kAtStages = 2;     // tiles in a warp's ring
-constexpr float kAtTop = 12.0f;  // log2 of the largest weight when the reference is set
-constexpr float kAtSlack = 3.0f; // a maximum may exceed that by this much before the reference moves
 constexpr int kAtUnit = 64;      // slots in a unit of work
-constexpr int kAtMinCost = 4;    // units a CTA takes at least
 // Starting a job costs about as much as this many units (its queries, its first pages and tiles,
-// the merge of its warps: 4 us beside 1.1 us a unit with the GPU full), and counts as such when the
-// work is divided.
+// the merge of its warps: 4 us beside 1.1 us a unit with the GPU full).
 constexpr int kAtJobUnits = 4;
-// A job (request or request row, key/value head, chunk of query rows) is split over CTAs
-// unless whole jobs cost at most this many units more on the busiest CTA; the combining
-// launch costs about as much.
+// A job is split unless whole jobs cost at most this many units more on the busiest CTA: the
+// joining launch costs about as much.
 constexpr int kAtSplitGain = 12;
 
 // ------------------------------------------------------------------------ small helpers
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ float lg2(float x) {
-    float y;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Value scales that their logarithm stands for: positive and neither tiny nor huge.  The others
-// count as 2^-100 .. 2^100 in the reference, times a ratio.
-__device__ __forceinline__ bool in_log_range(float v) { return v >= 7.888609e-31f && v <= 1.2676506e30f; }
-__device__ __forceinline__ float scale_log2(float v) { return fminf(fmaxf(lg2(fabsf(v)), -100.0f), 100.0f); }
-
-// Four e4m3 codes as two pairs of f16 (exact).
-__device__ __forceinline__ void codes_to_f16(uint32_t c, uint32_t& lo, uint32_t& hi) {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(c));
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-    return r;
-}
-
-__device__ __forceinline__ float2 unpack_f16(uint32_t u) {
-    return __half22float2(*reinterpret_cast<const __half2*>(&u));
-}
-
 // D += A B, A 16 x 16 row-major, B 16 x 8 column-major, f16 in, fp32 sums.
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint4 a, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -108,21 +60,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     uint2 v;
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
     return v;
-}
-
-template <typename T> __device__ __forceinline__ float to_f(T x);
-template <> __device__ __forceinline__ float to_f(float x) { return x; }
-template <> __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <> __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-
-__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__half* p, float4 v) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_f16(v.x, v.y), pack_f16(v.z, v.w));
-}
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-    *reinterpret_cast<uint2*>(p) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
 // -------------------------------------------------------------------- shared-memory tiles
@@ -169,70 +106,6 @@ template <int D> __device__ __forceinline__ int merge_at(int row, int f) {
     else return (f & ~7) | ((f & 7) ^ (((f >> 3) & 3) + 4 * (row & 1)));
 }
 
-// ------------------------------------------------------------------------- work division
-// A job is a (request, or with a list request row; key/value head; chunk of query rows).  Its cost
-// is kAtJobUnits and then its units of slots.  A split launch lays the requests' costs end to end
-// and divides them evenly into ranks; `per` CTAs, one for each head and chunk, share a rank, so
-// that a page's heads, which lie side by side, are read at about the same time.
-struct AtPlan {
-    int split;      // jobs may be divided over ranks; else CTAs take whole jobs
-    int mchunks;    // chunks of query rows per key/value head
-    int per;        // jobs of a request: kv_heads * mchunks
-    int n_virtual;  // requests, or with lists request rows
-    int by_job;     // `owner` has an entry per job, else one per CTA
-    float* rec;     // partial results: two records per CTA
-    int4* owner;    // a divided job (request, job of the request), its first rank and number of pieces (by_job:
-                    // of this job; else: of the job that this CTA begins and does not finish); w = 0: none
-};
-
-// Slots of request b's longest row (its own row's with a list); bad lengths count as 0.
-__device__ __forceinline__ int row_slots(const KvAttendArgs& a, int64_t br, int max_slots) {
-    const int n = a.n_slots[br];
-    if (n < 0 || n > max_slots) {
-        set_status(a.status, SPIN_STATUS_BAD_N);
-        return 0;
-    }
-    return n;
-}
-
-template <bool SPARSE>
-__device__ __forceinline__ int virtual_len(const spin_kv_config& cfg, const KvAttendArgs& a, int v) {
-    if constexpr (SPARSE) {
-        return row_slots(a, v, cfg.max_slots) > 0 ? a.top_k : 0;
-    } else {
-        int n = 0;
-        for (int r = 0; r < a.rows; ++r) n = max(n, row_slots(a, (int64_t)v * a.rows + r, cfg.max_slots));
-        return n;
-    }
-}
-
-__device__ __forceinline__ int64_t warp_incl_scan64(int64_t v) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t t = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += t;
-    }
-    return v;
-}
-
-// Inclusive scan over the CTA; *total is the sum.
-__device__ __forceinline__ int64_t cta_incl_scan64(int64_t v, int64_t* smem, int64_t* total) {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    int64_t s = warp_incl_scan64(v);
-    if (lane == 31) smem[w] = s;
-    __syncthreads();
-    int64_t all = 0;
-#pragma unroll
-    for (int i = 0; i < kAtWarps; ++i) {
-        if (i < w) s += smem[i];
-        all += smem[i];
-    }
-    __syncthreads();
-    *total = all;
-    return s;
-}
-
 // CTAs on an SM: three where registers and shared memory allow
 template <int D, int MT, bool SPLIT> constexpr int at_ctas() { return D == 256 ? 1 : MT == 2 || (SPLIT && D == 128) ? 2 : 3; }
 
@@ -257,101 +130,20 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
     const int H = cfg.n_heads, kvh = cfg.kv_heads, d = cfg.head_dim, group = H / kvh;
     const int rows = SPARSE ? 1 : a.rows, M = group * rows;
-    const int me = blockIdx.x, mine_of = me % plan.per, rank = me / plan.per;
     const float ninf = __uint_as_float(0xff800000u);
 
-    // this CTA's part of the work: [begin, end) of all requests' cost (split), or jobs me,
-    // me + gridDim.x, ... whole
-    int64_t total = 0, begin = 0, end = 0, ranks = gridDim.x / plan.per;
-    int v = 0;             // request the part begins in
-    int64_t into = 0;      // cost of that request before it
-    int len_v = -1;        // that request's slots, -1: not known yet
-    auto cost = [&](int len) -> int64_t { return len ? (len + kAtUnit - 1) / kAtUnit + kAtJobUnits : 0; };
-    if (plan.split) {
-        const bool one = plan.n_virtual <= kAtThreads;  // the first pass has every request's place
-        int len = 0;
-        int64_t inc = 0, sum;
-        for (int base = 0; base < plan.n_virtual; base += kAtThreads) {
-            const int x = base + tid;
-            len = x < plan.n_virtual ? virtual_len<SPARSE>(cfg, a, x) : 0;
-            inc = cta_incl_scan64(cost(len), sScan, &sum);
-            total += sum;
-        }
-        // every rank that takes part has some cost at least: a divided job's pieces are those of
-        // consecutive ranks
-        ranks = min(ranks, (total + kAtMinCost - 1) / kAtMinCost);
-        if (rank < ranks) {
-            begin = total * rank / ranks;
-            end = total * (rank + 1) / ranks;
-            int64_t before = 0;
-            for (int base = 0; base < plan.n_virtual; base += kAtThreads) {
-                const int x = base + tid;
-                if (!one) {
-                    len = x < plan.n_virtual ? virtual_len<SPARSE>(cfg, a, x) : 0;
-                    inc = before + cta_incl_scan64(cost(len), sScan, &sum);
-                    before += sum;
-                }
-                if (inc > begin && inc - cost(len) <= begin) {
-                    sScan[8] = x;
-                    sScan[9] = begin - (inc - cost(len));
-                    sScan[10] = len;
-                }
-                if (before > begin) break;
-            }
-            __syncthreads();
-            v = (int)sScan[8];
-            into = sScan[9];
-            len_v = (int)sScan[10];
-        }
-        if (tid == 0 && !plan.by_job) plan.owner[me].w = 0;
-    }
-
-    int64_t job = me;   // whole jobs
-    for (int64_t at = begin;;) {
-        // ---- the next segment: job (v, g, mc), units [u0, u1) of its `units`
-        int g, mc, len, units, u0, u1;
-        int64_t span = 0, first = 0, mine = 0;  // the job's cost, where this CTA enters it, how much it takes
-        if (plan.split) {
-            if (at >= end) break;
-            for (;;) {
-                if (len_v < 0) len_v = virtual_len<SPARSE>(cfg, a, v);
-                if (into < cost(len_v)) break;
-                into = 0;
-                len_v = -1;
-                ++v;
-            }
-            len = len_v;
-            units = (len + kAtUnit - 1) / kAtUnit;
-            span = units + kAtJobUnits;
-            g = mine_of / plan.mchunks;
-            mc = mine_of % plan.mchunks;
-            first = into;
-            mine = min(span - first, end - at);
-            u0 = (int)max((int64_t)0, first - kAtJobUnits);
-            u1 = (int)max((int64_t)0, first + mine - kAtJobUnits);
-            if (u0 == u1) {  // the part ends before the job's first unit
-                at += mine;
-                into += mine;
-                continue;
-            }
-        } else {
-            if (job >= (int64_t)plan.n_virtual * plan.per) break;
-            v = (int)(job / plan.per);
-            g = (int)(job % plan.per / plan.mchunks);
-            mc = (int)(job % plan.mchunks);
-            job += gridDim.x;
-            len = virtual_len<SPARSE>(cfg, a, v);
-            if (len == 0) continue;
-            units = (len + kAtUnit - 1) / kAtUnit;
-            u0 = 0;
-            u1 = units;
-        }
+    AtWalk<SPARSE> walk;
+    walk.template start<kAtWarps>(cfg, a, plan, sScan);
+    AtSegment seg;
+    while (walk.next(cfg, a, plan, seg)) {
+        const int v = seg.v, g = seg.g, len = seg.len;
         const int64_t b = SPARSE ? v / a.rows : v;
         const int64_t br0 = SPARSE ? v : (int64_t)v * a.rows;  // first (request, row)
-        const int m0 = mc * L::kRows, mrows = min(L::kRows, M - m0);
+        const int m0 = seg.mc * L::kRows, mrows = min(L::kRows, M - m0);
 
         // ---- this warp's tiles: tile0 + wid, + kAtWarps, ... below tile1
-        const int tile0 = u0 * (kAtUnit / kAtTile), tile1 = min(u1 * (kAtUnit / kAtTile), (len + kAtTile - 1) / kAtTile);
+        const int tile0 = seg.u0 * (kAtUnit / kAtTile);
+        const int tile1 = min(seg.u1 * (kAtUnit / kAtTile), (len + kAtTile - 1) / kAtTile);
         const int nt = max(0, (tile1 - tile0 - wid + kAtWarps - 1) / kAtWarps);
         const uint32_t ring = smem_u32(smem) + (uint32_t)(wid * kAtStages * St::kBytes);
         const int32_t* table = a.block_table + b * a.bt_stride;
@@ -791,7 +583,7 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
             __syncwarp();
             issue(k + kAtStages);
         }
-        if (plan.split ? at + mine >= end : job >= (int64_t)plan.n_virtual * plan.per) pdl_trigger();
+        if (walk.done(plan)) pdl_trigger();
         cp_wait<0>();
         __syncthreads();   // the ring is free: the warps' results go there
 
@@ -822,9 +614,9 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
                         }
             }
         __syncthreads();
-        const bool whole = u0 == 0 && u1 == units;
-        float* rec = nullptr;
-        if (!whole) rec = plan.rec + (int64_t)(2 * me + (u0 == 0 ? 1 : 0)) * L::kRows * (D + 2);
+        const bool whole = seg.u0 == 0 && seg.u1 == seg.units;
+        float* rec = AtWalk<SPARSE>::record(plan, seg, D);
+        if (tid == 0) walk.own(plan, seg);
         for (int e = tid; e < mrows * (D / 4); e += kAtThreads) {
             const int m = e / (D / 4), f = e % (D / 4);
             float top = ninf;
@@ -852,7 +644,7 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
                 if (4 * f < d)
                     store4(reinterpret_cast<T*>(a.out) + bh * d + 4 * f,
                            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-                if (a.lse && f == 0) a.lse[bh] = l == 0.0f ? ninf : ((top == ninf ? 0.0f : top) + log2f(l)) * 0.6931471805599453f;
+                if (a.lse && f == 0) a.lse[bh] = row_lse(top, l);
             } else {
                 reinterpret_cast<float4*>(rec + m * D)[f] = acc;
                 if (f == 0) {
@@ -861,140 +653,9 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
                 }
             }
         }
-        if (plan.split) {
-            if (tid == 0 && u0 == 0) {
-                int4 own = make_int4(v, mine_of, rank, 0);
-                if (u1 < units) {  // up to the rank that holds the end of the job's cost
-                    const int64_t last = at - first + span - 1;
-                    int64_t c = last * ranks / total;
-                    while (total * (c + 1) / ranks <= last) ++c;
-                    while (total * c / ranks > last) --c;
-                    own.w = (int)(c - rank) + 1;
-                }
-                if (plan.by_job) plan.owner[(int64_t)v * plan.per + mine_of] = own;
-                else if (own.w) plan.owner[me] = own;
-            }
-            at += mine;
-            into += mine;
-        }
         __syncthreads();
     }
-
-    // requests without any slot: zeros
-    for (int x = me; x < plan.n_virtual; x += gridDim.x) {
-        if (virtual_len<SPARSE>(cfg, a, x) > 0) continue;
-        const int64_t base = (int64_t)x * rows * H;
-        for (int64_t e = tid; e < (int64_t)rows * H * d / 4; e += kAtThreads)
-            store4(reinterpret_cast<T*>(a.out) + base * d + 4 * e, make_float4(0, 0, 0, 0));
-        if (a.lse)
-            for (int e = tid; e < rows * H; e += kAtThreads) a.lse[base + e] = ninf;
-        if (plan.split && plan.by_job)
-            for (int e = tid; e < plan.per; e += kAtThreads) plan.owner[(int64_t)x * plan.per + e].w = 0;
-    }
-}
-
-// Joins the pieces of the jobs that were divided: its first rank's second record, then the first
-// records of the ranks after it.  One CTA per job and query row: the pieces' factors first, then
-// each warp adds up every fourth piece.
-constexpr int kJoinWarps = 4;
-
-template <typename T, int D, int MT>
-__global__ void __launch_bounds__(32 * kJoinWarps)
-kv_attend_join_kernel(spin_kv_config cfg, KvAttendArgs a, AtPlan plan, int rows) {
-    pdl_wait();
-    constexpr int ROWS = 16 * MT, REC = ROWS * (D + 2), F = D / 32;
-    __shared__ float s_c[kAtMostPieces], s_w[kAtMostPieces], s_top[kJoinWarps], s_l[kJoinWarps];
-    __shared__ __align__(16) float s_acc[kJoinWarps][D];
-    const int4 job = plan.owner[blockIdx.x];
-    if (job.w == 0) return;
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, H = cfg.n_heads, d = cfg.head_dim;
-    const int group = H / cfg.kv_heads, g = job.y / plan.mchunks, m0 = job.y % plan.mchunks * ROWS, m = blockIdx.y;
-    const int pieces = job.w;
-    if (m >= min(ROWS, group * rows - m0)) return;
-    const float ninf = __uint_as_float(0xff800000u);
-    // CTA c has records 2c and 2c + 1; piece p lies in the first record of rank job.z + p, the first
-    // piece in the second of its rank
-    const float* rec = plan.rec + (int64_t)2 * (job.z * plan.per + job.y) * REC;
-    const int64_t step = (int64_t)2 * plan.per * REC;
-    auto at = [&](int p) -> const float* { return rec + (p ? p * step : REC); };
-    // a warp's first pieces are on their way while the factors are found
-    constexpr int AHEAD = 16 / F;
-    float x[AHEAD][F];
-    auto load = [&](float (&to)[F], int p) {
-        const float* r = at(p) + m * D + lane * F;
-        if constexpr (F == 2) {
-            const float2 y = *reinterpret_cast<const float2*>(r);
-            to[0] = y.x; to[1] = y.y;
-        } else {
-#pragma unroll
-            for (int i = 0; i < F; i += 4) {
-                const float4 y = *reinterpret_cast<const float4*>(r + i);
-                to[i] = y.x; to[i + 1] = y.y; to[i + 2] = y.z; to[i + 3] = y.w;
-            }
-        }
-    };
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k)
-        if (wid + k * kJoinWarps < pieces) load(x[k], wid + k * kJoinWarps);
-    float top = ninf, l = 0.0f;
-    for (int p = tid; p < pieces; p += 32 * kJoinWarps) {
-        const float2 ml = *reinterpret_cast<const float2*>(at(p) + ROWS * D + 2 * m);
-        s_c[p] = ml.x;
-        s_w[p] = ml.y;
-        top = fmaxf(top, ml.x);
-    }
-#pragma unroll
-    for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
-    if (lane == 0) s_top[wid] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_top[w]);
-    for (int p = tid; p < pieces; p += 32 * kJoinWarps) {
-        const float c = s_c[p] == ninf ? 0.0f : ex2(s_c[p] - top);
-        s_c[p] = c;
-        l = fmaf(c, s_w[p], l);
-    }
-#pragma unroll
-    for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
-    if (lane == 0) s_l[wid] = l;
-    __syncthreads();
-    l = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) l += s_l[w];
-    float acc[F];
-#pragma unroll
-    for (int i = 0; i < F; ++i) acc[i] = 0.0f;
-    for (int base = wid; base < pieces; base += AHEAD * kJoinWarps) {
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            const int p = base + k * kJoinWarps;
-            if (p >= pieces) break;
-            const float c = s_c[p];
-#pragma unroll
-            for (int i = 0; i < F; ++i) acc[i] = fmaf(c, x[k][i], acc[i]);
-        }
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            const int p = base + (AHEAD + k) * kJoinWarps;
-            if (p < pieces) load(x[k], p);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < F; ++i) s_acc[wid][lane * F + i] = acc[i];
-    __syncthreads();
-    const int64_t bh = ((int64_t)job.x * rows + (m0 + m) / group) * H + (int64_t)g * group + (m0 + m) % group;
-    const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-    for (int f = tid; f < d / 4; f += 32 * kJoinWarps) {
-        float4 y = make_float4(0, 0, 0, 0);
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) {
-            const float4 x = *reinterpret_cast<const float4*>(&s_acc[w][4 * f]);
-            y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
-        }
-        if (l == 0.0f) y = make_float4(0, 0, 0, 0);
-        store4(reinterpret_cast<T*>(a.out) + bh * d + 4 * f, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
-    }
-    if (a.lse && tid == 0) a.lse[bh] = l == 0.0f ? ninf : ((top == ninf ? 0.0f : top) + log2f(l)) * 0.6931471805599453f;
+    write_empty<T, SPARSE>(cfg, a, plan);
 }
 
 // ------------------------------------------------------------------------------ host side
@@ -1003,11 +664,13 @@ static int at_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 // output leaves registers for one
 static int at_mtiles(int D, int M) { return M > 16 && D <= 128 ? 2 : 1; }
 
-// Two records for every CTA of any variant.
+// Two records for every CTA of any variant (at most 32 rows each here).
 size_t kv_attend_workspace_bytes(const spin_kv_config& cfg, int, int) {
     const int D = at_dim(cfg.head_dim);
     const size_t G = kAtMostCtas * (size_t)device_sm_count();
-    return (G * sizeof(int4) + 255) / 256 * 256 + G * 2 * 32 * (size_t)(D + 2) * sizeof(float);
+    const size_t here = (G * sizeof(int4) + 255) / 256 * 256 + G * 2 * 32 * (size_t)(D + 2) * sizeof(float);
+    const size_t tc = kv_attend_tc_workspace_bytes(cfg);
+    return here > tc ? here : tc;
 }
 
 template <typename T, int D, int MT, bool SPARSE>
@@ -1022,6 +685,9 @@ static cudaError_t launch_at(const spin_kv_config& cfg, const KvAttendArgs& a, c
     p.mchunks = (M + L::kRows - 1) / L::kRows;
     p.n_virtual = SPARSE ? cfg.n_req * a.rows : cfg.n_req;
     p.per = cfg.kv_heads * p.mchunks;
+    p.unit = kAtUnit;
+    p.job_units = kAtJobUnits;
+    p.crows = L::kRows;
     const int64_t jobs = (int64_t)p.n_virtual * p.per;
     const int64_t most = ((SPARSE ? a.top_k : cfg.max_slots) + kAtUnit - 1) / kAtUnit;
     const int64_t ctas = at_ctas<D, MT, SPLIT>() * (int64_t)(device_sm_count() < kAtMostSms ? device_sm_count() : kAtMostSms);
@@ -1034,7 +700,7 @@ static cudaError_t launch_at(const spin_kv_config& cfg, const KvAttendArgs& a, c
     p.rec = a.workspace + ((size_t)kAtMostCtas * device_sm_count() * sizeof(int4) + 255) / 256 * 64;
     e = launch_pdl(k, dim3(G), dim3(kAtThreads), L::kBytes, s, nullptr, 0, cfg, a, p);
     if (e != cudaSuccess || !p.split) return e;
-    return launch_pdl(kv_attend_join_kernel<T, D, MT>, dim3(p.by_job ? (unsigned)jobs : G, M < L::kRows ? M : L::kRows),
+    return launch_pdl(kv_attend_join_kernel<T, D>, dim3(p.by_job ? (unsigned)jobs : G, M < L::kRows ? M : L::kRows),
                       dim3(32 * kJoinWarps), 0, s, nullptr, 0, cfg, a, p, SPARSE ? 1 : a.rows);
 }
 
@@ -1053,6 +719,7 @@ static cudaError_t launch_typed(const spin_kv_config& cfg, const KvAttendArgs& a
 }
 
 cudaError_t launch_kv_attend(const spin_kv_config& cfg, const KvAttendArgs& a, cudaStream_t s) {
+    if (kv_attend_tc_takes(cfg, a.rows, a.list != nullptr)) return launch_kv_attend_tc(cfg, a, s);
     switch (cfg.dtype) {
         case SPIN_DTYPE_F32: return launch_typed<float>(cfg, a, s);
         case SPIN_DTYPE_BF16: return launch_typed<__nv_bfloat16>(cfg, a, s);
