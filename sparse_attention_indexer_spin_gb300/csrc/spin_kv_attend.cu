@@ -41,21 +41,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint4 a, uint32_t b
         : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
-// 16 (or 4) bytes global -> shared, zeros instead where !live.
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool live) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-    return v;
-}
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
     uint2 v;
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
@@ -127,11 +112,13 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
     float* sM = reinterpret_cast<float*>(sN + L::kRows);
     float* sL = sM + kAtWarps * L::kRows;
     int64_t* sScan = reinterpret_cast<int64_t*>(sL + kAtWarps * L::kRows);
+    volatile int* sNan = reinterpret_cast<volatile int*>(sScan + 15);  // a NaN that only some rows see
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
     const int H = cfg.n_heads, kvh = cfg.kv_heads, d = cfg.head_dim, group = H / kvh;
     const int rows = SPARSE ? 1 : a.rows, M = group * rows;
     const float ninf = __uint_as_float(0xff800000u);
 
+    if (tid == 0) *sNan = 0;
     AtWalk<SPARSE> walk;
     walk.template start<kAtWarps>(cfg, a, plan, sScan);
     AtSegment seg;
@@ -496,47 +483,21 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
                 }
             }
 
-            // A NaN code that some rows see and others do not would reach the others as 0 x NaN:
-            // such codes turn the outputs of the rows that see them to NaN here and leave the tile.
+            // A NaN code that some rows see and others do not would reach the others as 0 x NaN: such codes
+            // leave the tile, and the rows that see them are looked for when the segment ends.
             if (!SPARSE && rows > 1 && slot0 + kAtTile > nmin) {
                 bool nan = false;
+#pragma unroll 1
                 for (int e = lane; e < kAtTile * D / 4; e += 32) {
                     uint32_t w;
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(st + St::kValues + 4 * e) : "memory");
-                    w &= 0x7f7f7f7fu;
-                    nan |= ((w + 0x01010101u) & 0x80808080u) != 0;
+                    const uint32_t at = st + St::kValues + 4 * e;
+                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+                    const uint32_t m = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // bytes that are NaN
+                    nan |= m != 0;
+                    if (m) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(w & ~((m >> 7) * 0xffu)) : "memory");
                 }
-                if (__any_sync(0xffffffffu, nan)) {
-                    for (int sl = 0; sl < kAtTile; ++sl) {
-                        const int slot = slot0 + sl;
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const int dim = D == 64 ? 8 * (2 * t4 + x) + n
-                                                        : 128 * (n >> 4) + 16 * (2 * t4 + x) + (n & 15);
-                                uint32_t c;
-                                asm volatile("ld.shared.u8 %0, [%1];"
-                                             : "=r"(c)
-                                             : "r"(st + St::kValues + value_at<D>(sl, dim >> 4) + (dim & 15))
-                                             : "memory");
-                                if ((c & 0x7fu) != 0x7fu) continue;
-#pragma unroll
-                                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                                    for (int r = 0; r < 2; ++r)
-                                        if (slot < nlim[i][r]) o[i][n][2 * r + x] = __uint_as_float(0x7fffffffu);
-                            }
-                    }
-                    __syncwarp();
-                    for (int e = lane; e < kAtTile * D; e += 32) {
-                        uint32_t c;
-                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(c) : "r"(st + St::kValues + e) : "memory");
-                        if ((c & 0x7fu) == 0x7fu)
-                            asm volatile("st.shared.u8 [%0], %1;" ::"r"(st + St::kValues + e), "r"(0) : "memory");
-                    }
-                    __syncwarp();
-                }
+                if (nan) *sNan = 1;
+                __syncwarp();
             }
 
             // ---- o += weights x values: column n of tile i holds dim 16 n + i (of each 128; D = 64:
@@ -624,6 +585,7 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
             for (int w = 0; w < kAtWarps; ++w) top = fmaxf(top, sM[w * L::kRows + m]);
             float l = 0.0f;
             float4 acc = make_float4(0, 0, 0, 0);
+            uint32_t nan_bits = 0;
 #pragma unroll
             for (int w = 0; w < kAtWarps; ++w) {
                 const float mw = sM[w * L::kRows + m];
@@ -636,6 +598,18 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
                 acc.y = fmaf(c, x.y, acc.y);
                 acc.z = fmaf(c, x.z, acc.z);
                 acc.w = fmaf(c, x.w, acc.w);
+            }
+            if (!SPARSE && *sNan) {
+                // (from the tile on in which the shortest row ends)
+                const int64_t br = br0 + (m0 + m) / group;
+                const int last = min(row_slots(a, br, cfg.max_slots), kAtUnit * seg.u1), first = max(nmin & ~(kAtTile - 1), kAtUnit * seg.u0);
+#pragma unroll 1
+                for (int k = 0; k < 4 && 4 * f + k < d; ++k)
+                    if (nan_value(cfg, a, v, g, 4 * f + k, first, last)) nan_bits |= 1u << k;
+                if (nan_bits & 1u) acc.x = __uint_as_float(0x7fffffffu);
+                if (nan_bits & 2u) acc.y = __uint_as_float(0x7fffffffu);
+                if (nan_bits & 4u) acc.z = __uint_as_float(0x7fffffffu);
+                if (nan_bits & 8u) acc.w = __uint_as_float(0x7fffffffu);
             }
             if (whole) {
                 const int64_t bh = (br0 + (m0 + m) / group) * H + (int64_t)g * group + (m0 + m) % group;
@@ -719,7 +693,7 @@ static cudaError_t launch_typed(const spin_kv_config& cfg, const KvAttendArgs& a
 }
 
 cudaError_t launch_kv_attend(const spin_kv_config& cfg, const KvAttendArgs& a, cudaStream_t s) {
-    if (kv_attend_tc_takes(cfg, a.rows, a.list != nullptr)) return launch_kv_attend_tc(cfg, a, s);
+    if (kv_attend_tc_takes(cfg, a.rows, a.list != nullptr, a.n_pages)) return launch_kv_attend_tc(cfg, a, s);
     switch (cfg.dtype) {
         case SPIN_DTYPE_F32: return launch_typed<float>(cfg, a, s);
         case SPIN_DTYPE_BF16: return launch_typed<__nv_bfloat16>(cfg, a, s);

@@ -50,6 +50,21 @@ __device__ __forceinline__ float2 unpack_f16(uint32_t u) {
     return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
 
+// 16 (or 4) bytes global -> shared, zeros instead where !live.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(live ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
 template <typename T> __device__ __forceinline__ float to_f(T x);
 template <> __device__ __forceinline__ float to_f(float x) { return x; }
 template <> __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -273,7 +288,7 @@ template <bool SPARSE> struct AtWalk {
 
 // Requests without any slot: zeros.
 template <typename T, bool SPARSE>
-__device__ __forceinline__ void write_empty(const spin_kv_config& cfg, const KvAttendArgs& a, const AtPlan& plan) {
+__device__ __noinline__ void write_empty(const spin_kv_config& cfg, const KvAttendArgs& a, const AtPlan& plan) {
     const int rows = SPARSE ? 1 : a.rows, H = cfg.n_heads, d = cfg.head_dim;
     for (int x = blockIdx.x; x < plan.n_virtual; x += gridDim.x) {
         if (virtual_len<SPARSE>(cfg, a, x) > 0) continue;
@@ -285,6 +300,18 @@ __device__ __forceinline__ void write_empty(const spin_kv_config& cfg, const KvA
         if (plan.split && plan.by_job)
             for (int e = threadIdx.x; e < plan.per; e += blockDim.x) plan.owner[(int64_t)x * plan.per + e].w = 0;
     }
+}
+
+// Whether a NaN value of dimension `dim` is among slots [first, last) of request b: the rare look
+// behind a NaN that only some of a job's rows see.
+static __device__ __noinline__ bool nan_value(const spin_kv_config& cfg, const KvAttendArgs& a, int64_t b, int g, int dim,
+                                              int first, int last) {
+    for (int s = first; s < last; ++s) {
+        const int p = a.block_table[b * a.bt_stride + (s >> 6)];
+        if (p < 0 || p >= a.n_pages) continue;
+        if ((a.v_pool[(((int64_t)p * kBlock + (s & 63)) * cfg.kv_heads + g) * cfg.head_dim + dim] & 0x7f) == 0x7f) return true;
+    }
+    return false;
 }
 
 // lse of a row from its reference and sum.
