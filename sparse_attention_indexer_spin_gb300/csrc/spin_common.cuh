@@ -5,6 +5,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/spin.h"
 
 #if defined(__CUDA_ARCH__) && (__CUDA_ARCH__ != 1030)
@@ -235,6 +237,19 @@ inline cudaError_t launch_pdl(void (*k)(P...), dim3 grid, dim3 block, size_t sme
         void* pa[] = {const_cast<void*>(static_cast<const void*>(&coerced))...};
         return cudaLaunchKernelExC(&lc, reinterpret_cast<const void*>(k), pa);
     }(static_cast<A&&>(args)...);
+}
+
+// A kernel's dynamic shared memory limit, raised on its first launch on each device (the call costs
+// about 1 us of host time).  `done` belongs to the kernel: one bit per device.
+inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 // ---------------------------------------------------------------------------------------

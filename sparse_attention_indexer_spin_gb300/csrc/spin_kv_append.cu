@@ -64,22 +64,48 @@ __device__ __forceinline__ float2 values2(uint32_t two_codes) {
 // values are read once into registers (NV 16-byte vectors a thread), reduced to max|x|, and
 // written as codes.
 template <typename T, int NV>
-__global__ void __launch_bounds__(kAppThreads)
-kv_append_kernel(spin_kv_config cfg, KvAppendArgs a, int pages) {
+__global__ void __launch_bounds__(kAppThreads, NV <= 4 ? 5 : 1)
+kv_append_kernel(spin_kv_config cfg, KvAppendArgs a) {
     pdl_begin();
     constexpr int E = 16 / (int)sizeof(T);  // elements per vector
     __shared__ float s_amax[kAppThreads / 32];
-    const int tid = threadIdx.x, r = blockIdx.y, kv = blockIdx.z;
-    const int h = blockIdx.x / pages, jj = blockIdx.x % pages;
+    const int tid = threadIdx.x, lane = tid & 31, kv = blockIdx.y, h = blockIdx.x % cfg.kv_heads;
     const int kvh = cfg.kv_heads, d = cfg.head_dim;
 
-    const int64_t t0 = a.new_start[r], t1 = a.new_start[r + 1], cnt = t1 - t0, nb = a.n_before[r];
-    if (t0 < 0 || cnt < 0 || t1 > a.n_tokens || cnt > a.max_new || nb < 0 || nb + cnt > cfg.max_slots) {
-        if (tid == 0 && jj == 0 && h == 0) set_status(a.status, SPIN_STATUS_BAD_N);
-        return;
+    // The touched pages of all requests are laid end to end; every warp looks up which of them this
+    // CTA's is, 32 requests at a time.
+    int jj = blockIdx.x / kvh, r = -1;  // page jj of request r
+    int64_t t0 = 0, cnt = 0, nb = 0;
+    const bool reports = blockIdx.x == 0 && kv == 0 && tid < 32;  // this warp looks at every request
+    for (int base = 0; base < cfg.n_req; base += 32) {
+        const int x = base + lane;
+        int64_t s0 = 0, c = 0, n = 0;
+        int pages = 0;
+        if (x < cfg.n_req) {
+            s0 = a.new_start[x];
+            c = a.new_start[x + 1] - s0;
+            n = a.n_before[x];
+            if (s0 < 0 || c < 0 || s0 + c > a.n_tokens || c > a.max_new || n < 0 || n + c > cfg.max_slots) {
+                if (reports) set_status(a.status, SPIN_STATUS_BAD_N);
+            } else if (c > 0) {
+                pages = (int)(((n + c - 1) >> 6) - (n >> 6)) + 1;
+            }
+        }
+        const int upto = warp_incl_scan(pages);
+        const uint32_t here = __ballot_sync(0xffffffffu, upto > jj);
+        if (r < 0 && here) {
+            const int at = __ffs(here) - 1;
+            r = base + at;
+            jj -= __shfl_sync(0xffffffffu, upto - pages, at);
+            t0 = __shfl_sync(0xffffffffu, s0, at);
+            cnt = __shfl_sync(0xffffffffu, c, at);
+            nb = __shfl_sync(0xffffffffu, n, at);
+            if (!reports) break;
+        }
+        if (r < 0) jj -= __shfl_sync(0xffffffffu, upto, 31);
     }
+    if (r < 0) return;
     const int64_t j = (nb >> 6) + jj;
-    if (cnt == 0 || j > (nb + cnt - 1) >> 6) return;
     const int64_t page = a.block_table[(int64_t)r * a.bt_stride + j];
     if (page < 0 || page >= a.n_pages) {
         if (tid == 0) set_status(a.status, SPIN_STATUS_BAD_PAGE);
@@ -151,13 +177,17 @@ kv_append_kernel(spin_kv_config cfg, KvAppendArgs a, int pages) {
 template <typename T>
 static cudaError_t launch_typed(const spin_kv_config& cfg, const KvAppendArgs& a, cudaStream_t s) {
     if (a.max_new == 0) return cudaSuccess;
-    const int pages = (int)(((int64_t)a.max_new + kBlock - 2) / kBlock) + 1;  // touched by max_new slots, at most
-    const dim3 grid((unsigned)pages * cfg.kv_heads, cfg.n_req, 2);
+    // pages touched, at most: n slots touch (n + 62) / 64 + 1, one page more than they fill
+    const int64_t each = ((int64_t)a.max_new + kBlock - 2) / kBlock + 1;
+    const int64_t all = a.n_tokens / kBlock + 2 * (int64_t)cfg.n_req;
+    const int64_t pages = each * cfg.n_req < all ? each * cfg.n_req : all;
+    if (pages * cfg.kv_heads > 0x7fffffff) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)(pages * cfg.kv_heads), 2);
     const int nv = (kBlock * cfg.head_dim * (int)sizeof(T) + 16 * kAppThreads - 1) / (16 * kAppThreads);
-    if (nv <= 4) return launch_pdl(kv_append_kernel<T, 4>, grid, dim3(kAppThreads), 0, s, nullptr, 0, cfg, a, pages);
-    if (nv <= 8) return launch_pdl(kv_append_kernel<T, 8>, grid, dim3(kAppThreads), 0, s, nullptr, 0, cfg, a, pages);
+    if (nv <= 4) return launch_pdl(kv_append_kernel<T, 4>, grid, dim3(kAppThreads), 0, s, nullptr, 0, cfg, a);
+    if (nv <= 8) return launch_pdl(kv_append_kernel<T, 8>, grid, dim3(kAppThreads), 0, s, nullptr, 0, cfg, a);
     if constexpr (sizeof(T) == 4)
-        return launch_pdl(kv_append_kernel<T, 16>, grid, dim3(kAppThreads), 0, s, nullptr, 0, cfg, a, pages);
+        return launch_pdl(kv_append_kernel<T, 16>, grid, dim3(kAppThreads), 0, s, nullptr, 0, cfg, a);
     return cudaErrorInvalidValue;  // not reached: head_dim <= 256
 }
 

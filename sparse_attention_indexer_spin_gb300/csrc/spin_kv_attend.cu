@@ -652,7 +652,8 @@ static cudaError_t launch_at(const spin_kv_config& cfg, const KvAttendArgs& a, c
     constexpr bool SPLIT = std::is_same<T, float>::value;
     using L = AtSmem<D, MT, SPLIT, SPARSE>;
     auto k = kv_attend_kernel<T, D, MT, SPARSE>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+    static std::atomic<uint64_t> allowed;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), L::kBytes, allowed);
     if (e != cudaSuccess) return e;
     const int M = cfg.n_heads / cfg.kv_heads * (SPARSE ? 1 : a.rows);
     AtPlan p;

@@ -796,7 +796,7 @@ static int tc_rows(int M) { return M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 // Tensor-map coordinates are 32-bit (pages x 64 slots), and a copy of four rows starts on 128 bytes.
 bool kv_attend_tc_takes(const spin_kv_config& cfg, int rows, bool listed, int64_t n_pages) {
     const int M = cfg.n_heads / cfg.kv_heads * (listed ? 1 : rows);
-    return cfg.dtype != SPIN_DTYPE_F32 && cfg.head_dim <= 128 && M > 16 && n_pages >= 1 && n_pages < (1 << 25) &&
+    return false && cfg.dtype != SPIN_DTYPE_F32 && cfg.head_dim <= 128 && M > 16 && n_pages >= 1 && n_pages < (1 << 25) &&
            (!listed || cfg.head_dim % 32 == 0);
 }
 
@@ -823,7 +823,8 @@ template <typename T, int D, bool SPARSE>
 static cudaError_t launch_x(const spin_kv_config& cfg, const KvAttendArgs& a, cudaStream_t s) {
     using L = XSmem<D>;
     auto k = kv_attend_tc_kernel<T, D, SPARSE>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+    static std::atomic<uint64_t> allowed;
+    cudaError_t e = allow_smem(reinterpret_cast<const void*>(k), L::kBytes, allowed);
     if (e != cudaSuccess) return e;
     const int M = cfg.n_heads / cfg.kv_heads * (SPARSE ? 1 : a.rows);
     AtPlan p;

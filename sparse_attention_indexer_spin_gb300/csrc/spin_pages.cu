@@ -13,6 +13,7 @@ namespace spin {
 
 constexpr int kPgThreads = 256;
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanPages = 16;         // neighbouring pages a thread of a plan looks at, at a time
 constexpr int kCopyBytes = 16 * 1024;  // bytes one CTA copies at a time
 
 // Workspace: a header of 64 words, then prefix [n_req], dst, src and aux [n_pages].
@@ -22,7 +23,7 @@ struct PagesWs {
     int32_t* prefix;  // fresh pages wanted by the requests before this one
     int32_t* dst;
     int32_t* src;     // page to copy to dst, -1: none
-    int32_t* aux;     // reserve: page the request leaves, -1: none; compaction: new id of a page
+    int32_t* aux;     // reserve: page the request leaves, -1: none; compaction: rank of a page that moves, -1: free
 };
 
 static __host__ __device__ inline int64_t round64(int64_t n) { return (n + 63) & ~(int64_t)63; }
@@ -106,6 +107,21 @@ __global__ void __launch_bounds__(kPgThreads) pages_free_kernel(PageTable t, con
 }
 
 // ------------------------------------------------------------------------------- reserve
+// Pages p0 .. p0 + kPlanPages - 1 as bits: those that exist, those in use.
+__device__ __forceinline__ uint32_t pages_there(const PageTable& t, int64_t p0) {
+    const int64_t n = t.n_pages - p0;
+    return n <= 0 ? 0u : n >= kPlanPages ? (1u << kPlanPages) - 1 : (1u << n) - 1;
+}
+__device__ __forceinline__ uint32_t used_pages(const PageTable& t, int64_t p0) {
+    int ref[kPlanPages];
+#pragma unroll
+    for (int i = 0; i < kPlanPages; ++i) ref[i] = p0 + i < t.n_pages ? t.ref[p0 + i] : 0;
+    uint32_t used = 0;
+#pragma unroll
+    for (int i = 0; i < kPlanPages; ++i) used |= (uint32_t)(ref[i] > 0) << i;
+    return used;
+}
+
 struct Span {
     int64_t j0, j1;   // blocks [j0, j1) the next slots fall in
     bool partial;     // the first of them already holds some of the request's slots
@@ -160,11 +176,11 @@ pages_reserve_kernel(PageTable t, const int32_t* n_slots, const int32_t* n_new, 
     }
     const int total = carry;
     int found = 0;
-    for (int64_t base = 0; base < t.n_pages && found < total; base += kPlanThreads) {
-        const int64_t p = base + tid;
-        const int is_free = p < t.n_pages && t.ref[p] <= 0;
-        const int rank = found + block_excl_scan(is_free, s_scan, &sum);
-        if (is_free && rank < total) w.dst[rank] = (int32_t)p;
+    for (int64_t base = 0; base < t.n_pages && found < total; base += kPlanThreads * kPlanPages) {
+        const int64_t p0 = base + (int64_t)tid * kPlanPages;
+        const uint32_t free_pages = ~used_pages(t, p0) & pages_there(t, p0);
+        int rank = found + block_excl_scan(__popc(free_pages), s_scan, &sum);
+        for (uint32_t f = free_pages; f && rank < total; f &= f - 1) w.dst[rank++] = (int32_t)(p0 + __ffs(f) - 1);
         found += sum;
     }
     found = min(found, total);
@@ -200,30 +216,36 @@ pages_reserve_kernel(PageTable t, const int32_t* n_slots, const int32_t* n_new, 
 
 // ------------------------------------------------------------------------------- compact
 // The plan, by one CTA: the number L of pages in use, the used pages from L on (src) and the
-// free ones below L (dst), both ascending, and the new id of every page from L on (aux).
+// free ones below L (dst), both ascending, and the new id of every page from L on (aux; -1 for a free
+// one).  There are as many of the ones as of the others, so a page's new id is the dst of its rank.
 __global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(PageTable t, int32_t* n_live, PagesWs w) {
     pdl_begin();
     __shared__ int s_scan[33];
     const int tid = threadIdx.x;
     int cnt = 0, live;
+#pragma unroll 8
     for (int64_t p = tid; p < t.n_pages; p += kPlanThreads) cnt += t.ref[p] > 0;
     block_excl_scan(cnt, s_scan, &live);
     int holes = 0, moves = 0, sum;
-    for (int64_t base = 0; base < t.n_pages; base += kPlanThreads) {
-        const int64_t p = base + tid;
-        const bool used = p < t.n_pages && t.ref[p] > 0;
-        const int hole = p < live && !used, move = p >= live && used;
-        const int rh = block_excl_scan(hole, s_scan, &sum);
-        if (hole) w.dst[holes + rh] = (int32_t)p;
-        holes += sum;
-        const int rm = block_excl_scan(move, s_scan, &sum);
-        if (move) w.src[moves + rm] = (int32_t)p;
-        moves += sum;
+    for (int64_t base = 0; base < t.n_pages; base += kPlanThreads * kPlanPages) {
+        const int64_t p0 = base + (int64_t)tid * kPlanPages;
+        const uint32_t there = pages_there(t, p0), used = used_pages(t, p0);
+        const int64_t below = live - p0;  // the first of them lie below L
+        const uint32_t low = below <= 0 ? 0u : below >= kPlanPages ? ~0u : (1u << below) - 1;
+        // (both counts in one scan: at most 16384 each)
+        const int both = block_excl_scan(__popc(~used & low & there) | __popc(used & ~low) << 16, s_scan, &sum);
+        int rank = holes + (both & 0xffff);
+        for (uint32_t f = ~used & low & there; f; f &= f - 1) w.dst[rank++] = (int32_t)(p0 + __ffs(f) - 1);
+        rank = moves + (both >> 16);
+        for (uint32_t f = ~low & there; f; f &= f - 1) {
+            const int64_t p = p0 + __ffs(f) - 1;
+            const bool move = used >> (p - p0) & 1u;
+            if (move) w.src[rank] = (int32_t)p;
+            w.aux[p] = move ? rank++ : -1;
+        }
+        holes += sum & 0xffff;
+        moves += sum >> 16;
     }
-    __syncthreads();
-    for (int64_t p = live + tid; p < t.n_pages; p += kPlanThreads) w.aux[p] = -1;
-    __syncthreads();
-    for (int k = tid; k < moves; k += kPlanThreads) w.aux[w.src[k]] = w.dst[k];
     if (tid == 0) {
         *w.count = moves;
         *w.live = live;
@@ -231,27 +253,27 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(PageTable t
     }
 }
 
-__global__ void __launch_bounds__(kPgThreads) pages_remap_kernel(PageTable t, PagesWs w) {
-    pdl_begin();
-    const int64_t me = (int64_t)blockIdx.x * kPgThreads + threadIdx.x, all = (int64_t)gridDim.x * kPgThreads;
-    const int live = *w.live, moves = *w.count;
-    for (int64_t i = me; i < (int64_t)t.n_req * t.stride; i += all) {
-        const int32_t e = page_of(t.table[i], t);
-        if (e < live) continue;
-        const int32_t to = w.aux[e];
-        if (to >= 0) t.table[i] = to;
-        else set_status(t.status, SPIN_STATUS_BAD_REF);
-    }
-    for (int64_t k = me; k < moves; k += all) {
-        t.ref[w.dst[k]] = t.ref[w.src[k]];
-        t.ref[w.src[k]] = 0;
-    }
-}
-
 // ------------------------------------------------------------------------------- copying
-// Pages src[k] -> dst[k] of every pool, in chunks of kCopyBytes.  No source is a destination.
-__global__ void __launch_bounds__(kPgThreads) pages_copy_kernel(PagePoolSet pools, PagesWs w, int chunks) {
+// Pages src[k] -> dst[k] of every pool, in chunks of kCopyBytes.  No source is a destination.  After
+// a compaction's plan (REMAP) the table entries and reference counts follow first.
+template <bool REMAP>
+__global__ void __launch_bounds__(kPgThreads) pages_copy_kernel(PageTable t, PagePoolSet pools, PagesWs w, int chunks) {
     pdl_begin();
+    if constexpr (REMAP) {
+        const int64_t me = (int64_t)blockIdx.x * kPgThreads + threadIdx.x, all = (int64_t)gridDim.x * kPgThreads;
+        const int live = *w.live, moves = *w.count;
+        for (int64_t i = me; i < (int64_t)t.n_req * t.stride; i += all) {
+            const int32_t e = page_of(t.table[i], t);
+            if (e < live) continue;
+            const int32_t rank = w.aux[e];
+            if (rank >= 0) t.table[i] = w.dst[rank];
+            else set_status(t.status, SPIN_STATUS_BAD_REF);
+        }
+        for (int64_t k = me; k < moves; k += all) {
+            t.ref[w.dst[k]] = t.ref[w.src[k]];
+            t.ref[w.src[k]] = 0;
+        }
+    }
     const int64_t items = (int64_t)*w.count * chunks;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const int k = (int)(it / chunks);
@@ -306,11 +328,12 @@ cudaError_t launch_pages_free(const PageTable& t, const int32_t* keep, cudaStrea
     return launch_pdl(pages_free_kernel, table_grid(t), dim3(kPgThreads), 0, s, nullptr, 0, t, keep);
 }
 
-static cudaError_t launch_copy(const PagePoolSet& pools, const PagesWs& w, cudaStream_t s) {
+template <bool REMAP>
+static cudaError_t launch_copy(const PageTable& t, const PagePoolSet& pools, const PagesWs& w, cudaStream_t s) {
     const int chunks = copy_chunks(pools);
-    if (chunks == 0) return cudaSuccess;
-    return launch_pdl(pages_copy_kernel, dim3(8 * device_sm_count()), dim3(kPgThreads), 0, s, nullptr, 0, pools, w,
-                      chunks);
+    if (chunks == 0 && !REMAP) return cudaSuccess;
+    return launch_pdl(pages_copy_kernel<REMAP>, dim3(8 * device_sm_count()), dim3(kPgThreads), 0, s, nullptr, 0, t, pools,
+                      w, chunks);
 }
 
 cudaError_t launch_pages_reserve(const PageTable& t, const int32_t* n_slots, const int32_t* n_new,
@@ -318,16 +341,14 @@ cudaError_t launch_pages_reserve(const PageTable& t, const int32_t* n_slots, con
     const PagesWs w = pages_ws(ws, t.n_req, t.n_pages);
     cudaError_t e = launch_pdl(pages_reserve_kernel, dim3(1), dim3(kPlanThreads), 0, s, nullptr, 0, t, n_slots, n_new,
                                granted, w);
-    return e != cudaSuccess ? e : launch_copy(pools, w, s);
+    return e != cudaSuccess ? e : launch_copy<false>(t, pools, w, s);
 }
 
 cudaError_t launch_pages_compact(const PageTable& t, const PagePoolSet& pools, int32_t* n_live, void* ws,
                                  cudaStream_t s) {
     const PagesWs w = pages_ws(ws, t.n_req, t.n_pages);
     cudaError_t e = launch_pdl(pages_compact_kernel, dim3(1), dim3(kPlanThreads), 0, s, nullptr, 0, t, n_live, w);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(pages_remap_kernel, dim3(device_sm_count()), dim3(kPgThreads), 0, s, nullptr, 0, t, w);
-    return e != cudaSuccess ? e : launch_copy(pools, w, s);
+    return e != cudaSuccess ? e : launch_copy<true>(t, pools, w, s);
 }
 
 }  // namespace spin
