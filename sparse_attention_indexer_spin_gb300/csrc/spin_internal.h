@@ -151,10 +151,6 @@ struct PagePoolSet {
 cudaError_t launch_kv_append(const spin_kv_config& cfg, const KvAppendArgs& a, cudaStream_t s);
 size_t kv_attend_workspace_bytes(const spin_kv_config& cfg, int rows, int top_k);
 cudaError_t launch_kv_attend(const spin_kv_config& cfg, const KvAttendArgs& a, cudaStream_t s);
-// The tcgen05 kernel, for many query rows per key/value head (spin_kv_attend_tc.cu).
-bool kv_attend_tc_takes(const spin_kv_config& cfg, int rows, bool listed, int64_t n_pages);
-size_t kv_attend_tc_workspace_bytes(const spin_kv_config& cfg);
-cudaError_t launch_kv_attend_tc(const spin_kv_config& cfg, const KvAttendArgs& a, cudaStream_t s);
 
 size_t pages_workspace_bytes(int32_t n_req, int64_t n_pages);
 cudaError_t launch_pages_fork(const PageTable& t, const int32_t* table_in, const int32_t* parent, cudaStream_t s);

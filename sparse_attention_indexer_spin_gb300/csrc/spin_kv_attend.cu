@@ -302,14 +302,19 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
 #pragma unroll
                         for (int w = 0; w < 4; ++w) qf[i][w] = sQ[(i * KS + 4 * c + w) * 32 + lane];
                 }
+                uint32_t kw[4][4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint4 kc = lds128(st + key_at<D>(8 * j + g8, 4 * c + t4));
-                    const uint32_t kw[4] = {kc.x, kc.y, kc.z, kc.w};
+                    kw[j][0] = kc.x, kw[j][1] = kc.y, kw[j][2] = kc.z, kw[j][3] = kc.w;
+                }
+                // (the column tiles' chains of products take turns)
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
+                for (int w = 0; w < 4; ++w)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
                         uint32_t b0, b1;
-                        codes_to_f16(kw[w], b0, b1);
+                        codes_to_f16(kw[j][w], b0, b1);
                         if constexpr (QREG) {
                             mma_f16(s[0][j], qr[4 * c + w], b0, b1);
                         } else {
@@ -320,7 +325,6 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
                             }
                         }
                     }
-                }
             }
 
             // ---- weights: 2^(t - m) vs, where t = qs ks s; with x = t + log2 vs they are 2^(x - m)
@@ -638,13 +642,11 @@ static int at_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 // output leaves registers for one
 static int at_mtiles(int D, int M) { return M > 16 && D <= 128 ? 2 : 1; }
 
-// Two records for every CTA of any variant (at most 32 rows each here).
+// Two records for every CTA of any variant, 32 rows each at most.
 size_t kv_attend_workspace_bytes(const spin_kv_config& cfg, int, int) {
     const int D = at_dim(cfg.head_dim);
     const size_t G = kAtMostCtas * (size_t)device_sm_count();
-    const size_t here = (G * sizeof(int4) + 255) / 256 * 256 + G * 2 * 32 * (size_t)(D + 2) * sizeof(float);
-    const size_t tc = kv_attend_tc_workspace_bytes(cfg);
-    return here > tc ? here : tc;
+    return (G * sizeof(int4) + 255) / 256 * 256 + G * 2 * 32 * (size_t)(D + 2) * sizeof(float);
 }
 
 template <typename T, int D, int MT, bool SPARSE>
@@ -694,7 +696,6 @@ static cudaError_t launch_typed(const spin_kv_config& cfg, const KvAttendArgs& a
 }
 
 cudaError_t launch_kv_attend(const spin_kv_config& cfg, const KvAttendArgs& a, cudaStream_t s) {
-    if (kv_attend_tc_takes(cfg, a.rows, a.list != nullptr, a.n_pages)) return launch_kv_attend_tc(cfg, a, s);
     switch (cfg.dtype) {
         case SPIN_DTYPE_F32: return launch_typed<float>(cfg, a, s);
         case SPIN_DTYPE_BF16: return launch_typed<__nv_bfloat16>(cfg, a, s);
