@@ -119,7 +119,8 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
     const float ninf = __uint_as_float(0xff800000u);
 
     if (tid == 0) *sNan = 0;
-    AtWalk<SPARSE> walk;
+    using Walk = AtWalk<SPARSE, kAtUnit, kAtJobUnits>;
+    Walk walk;
     walk.template start<kAtWarps>(cfg, a, plan, sScan);
     AtSegment seg;
     while (walk.next(cfg, a, plan, seg)) {
@@ -210,45 +211,49 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
             }
             cp_commit();
         };
-#pragma unroll
+#pragma unroll 1
         for (int k = 0; k < kAtStages; ++k) issue(k);
 
         // ---- queries: row m is (row m / group, head g * group + m % group), scaled by a power
         // of two and rounded to f16, laid out as the fragments read them
-        for (int m = wid; m < L::kRows; m += kAtWarps) {
-            const int64_t br = br0 + (m0 + m) / group;
-            const T* qp = reinterpret_cast<const T*>(a.q) + (br * H + (int64_t)g * group + (m0 + m) % group) * d;
-            float x[D / 32], amax = 0.0f;
+        // (16 neighbouring values a thread, D / 16 threads a row)
+#pragma unroll 1
+        for (int it = tid; it < L::kRows * (D / 16); it += kAtThreads) {
+            const int m = it / (D / 16), ch = it % (D / 16);
+            const int mr = (m0 + m) / group;
+            const int64_t br = br0 + mr;
+            const uint4* qp = reinterpret_cast<const uint4*>(reinterpret_cast<const T*>(a.q) +
+                                                             (br * H + (int64_t)g * group + (m0 + m - mr * group)) * d + 16 * ch);
+            constexpr int QN = 16 * (int)sizeof(T) / 16;
+            uint4 qv[QN];
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const int c = lane * (D / 32) + i;
-                x[i] = m < mrows && c < d ? to_f(qp[c]) : 0.0f;
+            for (int k = 0; k < QN; ++k) qv[k] = m < mrows && 16 * ch < d ? qp[k] : make_uint4(0, 0, 0, 0);
+            float x[16], amax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                x[i] = to_f(reinterpret_cast<const T*>(qv)[i]);
                 amax = fmaxf(amax, fabsf(x[i]));
             }
 #pragma unroll
-            for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            for (int o = D / 32; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
             // amax in [2^k, 2^(k+1)) -> [2^14, 2^15); 2^(14 - k) within [2^-113, 2^126]
             const int k = max(-112, (int)(__float_as_uint(amax) >> 23) - 127);
             const float f = __uint_as_float((uint32_t)(127 + 14 - k) << 23);
-            if (lane == 0) {
+            if (ch == 0) {
                 sQs[m] = __uint_as_float((uint32_t)max(1, 127 - 14 + k) << 23) * (cfg.softmax_scale * 1.4426950408889634f);
-                int n = 0x7fffffff;
-                if (!SPARSE && m < mrows) n = row_slots(a, br, cfg.max_slots);
-                sN[m] = n;
+                sN[m] = !SPARSE && m < mrows ? row_slots(a, br, cfg.max_slots) : 0x7fffffff;
             }
             // dims 64c + 16t + 4s + {0, 1} of row m are the pair k = 2t of contraction step 4c + s,
-            // {2, 3} the pair k = 2t + 8
+            // {2, 3} the pair k = 2t + 8; here ch = 4c + t
+            uint32_t* to = reinterpret_cast<uint32_t*>(sQ) +
+                           (((m >> 4) * KS + (ch >> 2) * 4) * 32 + (m & 7) * 4 + (ch & 3)) * 4 + ((m & 15) >> 3);
 #pragma unroll
-            for (int i = 0; i < D / 32; i += 2) {
-                const int c = lane * (D / 32) + i;
-                const uint32_t hi = pack_f16(x[i] * f, x[i + 1] * f);
-                const int step = (c >> 6) * 4 + ((c >> 2) & 3), t = (c >> 4) & 3, pair = (c >> 1) & 1;
-                const int word = ((m & 15) >> 3) + 2 * pair, ln = (m & 7) * 4 + t;
-                uint32_t* at32 = reinterpret_cast<uint32_t*>(sQ) + (((m >> 4) * KS + step) * 32 + ln) * 4 + word;
-                *at32 = hi;
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t hi = pack_f16(x[2 * i] * f, x[2 * i + 1] * f);
+                to[(i >> 1) * 128 + 2 * (i & 1)] = hi;
                 if constexpr (SPLIT) {
                     const float2 h = unpack_f16(hi);
-                    at32[MT * KS * 128] = pack_f16(x[i] * f - h.x, x[i + 1] * f - h.y);
+                    to[MT * KS * 128 + (i >> 1) * 128 + 2 * (i & 1)] = pack_f16(x[2 * i] * f - h.x, x[2 * i + 1] * f - h.y);
                 }
             }
         }
@@ -580,8 +585,9 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
             }
         __syncthreads();
         const bool whole = seg.u0 == 0 && seg.u1 == seg.units;
-        float* rec = AtWalk<SPARSE>::record(plan, seg, D);
+        float* rec = Walk::record(plan, seg, D);
         if (tid == 0) walk.own(plan, seg);
+#pragma unroll 1
         for (int e = tid; e < mrows * (D / 4); e += kAtThreads) {
             const int m = e / (D / 4), f = e % (D / 4);
             float top = ninf;
@@ -662,8 +668,6 @@ static cudaError_t launch_at(const spin_kv_config& cfg, const KvAttendArgs& a, c
     p.mchunks = (M + L::kRows - 1) / L::kRows;
     p.n_virtual = SPARSE ? cfg.n_req * a.rows : cfg.n_req;
     p.per = cfg.kv_heads * p.mchunks;
-    p.unit = kAtUnit;
-    p.job_units = kAtJobUnits;
     p.crows = L::kRows;
     const int64_t jobs = (int64_t)p.n_virtual * p.per;
     const int64_t most = ((SPARSE ? a.top_k : cfg.max_slots) + kAtUnit - 1) / kAtUnit;
@@ -672,6 +676,7 @@ static cudaError_t launch_at(const spin_kv_config& cfg, const KvAttendArgs& a, c
     const int64_t ranks = ctas / p.per, most_ranks = p.n_virtual * (most + kAtJobUnits + kAtMinCost - 1) / kAtMinCost;
     p.split = ranks > 0 && (jobs + ctas - 1) / ctas * most > jobs * most / (ranks * p.per) + kAtSplitGain;
     const int G = (int)(p.split ? (most_ranks < ranks ? most_ranks : ranks) * p.per : jobs < ctas ? jobs : ctas);
+    p.ranks = G / p.per;
     p.by_job = jobs <= G;
     p.owner = reinterpret_cast<int4*>(a.workspace);
     p.rec = a.workspace + ((size_t)kAtMostCtas * device_sm_count() * sizeof(int4) + 255) / 256 * 64;

@@ -1,5 +1,9 @@
-// spin_kv_attend.cuh -- what the attention kernels over the 8-bit KV cache share: the numbers'
-// conversions, the division of the work over CTAs, and the join of divided jobs.
+// spin_kv_attend.cuh -- parts of the attention over the 8-bit KV cache: small helpers, the division of
+// the work over CTAs, and the join of divided jobs.
+//
+// What runs once per CTA or segment is kept small in code (loops not unrolled, divisions out of
+// line): its instructions are fetched cold, and with everything unrolled a CTA's first tile started
+// 8 us after its launch.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -82,18 +86,17 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
 
 // ------------------------------------------------------------------------- work division
 // A job is a (request, or with a list request row; key/value head; chunk of query rows), its work a
-// row of units of `unit` slots, its cost job_units and then its units.  A split launch lays the
+// row of units of UNIT slots, its cost JOB_UNITS and then its units.  A split launch lays the
 // requests' costs end to end and divides them evenly into ranks; `per` CTAs, one for each head and
 // chunk, share a rank, so that a page's heads, which lie side by side, are read at about the same
 // time.
 struct AtPlan {
     int split;      // jobs may be divided over ranks; else CTAs take whole jobs
-    int unit;       // slots in a unit
-    int job_units;  // what starting a job costs, in units
     int crows;      // query rows in a chunk
     int mchunks;    // chunks of query rows per key/value head
     int per;        // jobs of a request: kv_heads * mchunks
     int n_virtual;  // requests, or with lists request rows
+    int ranks;      // gridDim.x / per
     int by_job;     // `owner` has an entry per job, else one per CTA
     float* rec;     // partial results, two records per CTA: crows x D sums, then (reference, l) of each row
     int4* owner;    // a divided job (request, job of the request), its first rank and number of pieces (by_job:
@@ -121,6 +124,7 @@ __device__ __forceinline__ int virtual_len(const spin_kv_config& cfg, const KvAt
         return row_slots(a, v, cfg.max_slots) > 0 ? a.top_k : 0;
     } else {
         int n = 0;
+#pragma unroll 1
         for (int r = 0; r < a.rows; ++r) n = max(n, row_slots(a, (int64_t)v * a.rows + r, cfg.max_slots));
         return n;
     }
@@ -154,6 +158,26 @@ __device__ __forceinline__ int64_t cta_incl_scan64(int64_t v, int64_t* smem, int
     return s;
 }
 
+static __device__ __noinline__ int2 div_mod(int a, int b) { return make_int2(a / b, a % b); }
+// a / b for 0 <= a, 0 < b (a long division takes some 700 cycles, and few totals need one)
+static __device__ __noinline__ int64_t quotient(int64_t a, int64_t b) {
+    return (uint64_t)(a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
+// `total` cut into `ranks` parts that differ by one at most, the longer ones first.
+struct AtCut {
+    int64_t each, more;   // length of the shorter parts; how many are one longer
+    __device__ __forceinline__ void set(int64_t total, int64_t ranks) {
+        each = quotient(total, ranks);
+        more = total - each * ranks;
+    }
+    __device__ __forceinline__ int64_t begin(int64_t rank) const { return rank * each + min(rank, more); }
+    __device__ __forceinline__ int64_t rank_of(int64_t x) const {
+        const int64_t longer = more * (each + 1);
+        return x < longer ? quotient(x, each + 1) : more + quotient(x - longer, each);
+    }
+};
+
 // One segment of a CTA's work: units [u0, u1) of the job (v, g, mc).
 struct AtSegment {
     int v, g, mc, len, units, u0, u1;
@@ -161,12 +185,13 @@ struct AtSegment {
 };
 
 // A CTA's walk over its segments.
-template <bool SPARSE> struct AtWalk {
-    int64_t total, at, end, ranks, into, job;
-    int v, len_v, rank, mine;
+template <bool SPARSE, int UNIT, int JOB_UNITS> struct AtWalk {
+    int64_t total, at, end, ranks, into;
+    AtCut cut;
+    int job, v, len_v, rank, mine;
 
-    __device__ __forceinline__ static int64_t cost(int len, const AtPlan& plan) {
-        return len ? (len + plan.unit - 1) / plan.unit + plan.job_units : 0;
+    __device__ __forceinline__ static int64_t cost(int len) {
+        return len ? (len + UNIT - 1) / UNIT + JOB_UNITS : 0;
     }
 
     // By the whole CTA of WARPS warps; smem: WARPS + 3 words.
@@ -174,8 +199,9 @@ template <bool SPARSE> struct AtWalk {
     __device__ __forceinline__ void start(const spin_kv_config& cfg, const KvAttendArgs& a, const AtPlan& plan, int64_t* smem) {
         constexpr int THREADS = 32 * WARPS;
         const int tid = threadIdx.x;
-        rank = blockIdx.x / plan.per;
-        mine = blockIdx.x % plan.per;
+        const int2 place = div_mod(blockIdx.x, plan.per);
+        rank = place.x;
+        mine = place.y;
         total = at = end = into = 0;
         job = blockIdx.x;
         v = 0;
@@ -184,29 +210,32 @@ template <bool SPARSE> struct AtWalk {
         const bool one = plan.n_virtual <= THREADS;  // the first pass has every request's place
         int len = 0;
         int64_t inc = 0, sum;
+#pragma unroll 1
         for (int base = 0; base < plan.n_virtual; base += THREADS) {
             const int x = base + tid;
             len = x < plan.n_virtual ? virtual_len<SPARSE>(cfg, a, x) : 0;
-            inc = cta_incl_scan64<WARPS>(cost(len, plan), smem, &sum);
+            inc = cta_incl_scan64<WARPS>(cost(len), smem, &sum);
             total += sum;
         }
         // every rank that takes part has some cost at least: a divided job's pieces are those of
         // consecutive ranks
-        ranks = min((int64_t)(gridDim.x / plan.per), (total + kAtMinCost - 1) / kAtMinCost);
+        ranks = min((int64_t)plan.ranks, (total + kAtMinCost - 1) / kAtMinCost);
         if (rank < ranks) {
-            at = total * rank / ranks;
-            end = total * (rank + 1) / ranks;
+            cut.set(total, ranks);
+            at = cut.begin(rank);
+            end = cut.begin(rank + 1);
             int64_t before = 0;
+#pragma unroll 1
             for (int base = 0; base < plan.n_virtual; base += THREADS) {
                 const int x = base + tid;
                 if (!one) {
                     len = x < plan.n_virtual ? virtual_len<SPARSE>(cfg, a, x) : 0;
-                    inc = before + cta_incl_scan64<WARPS>(cost(len, plan), smem, &sum);
+                    inc = before + cta_incl_scan64<WARPS>(cost(len), smem, &sum);
                     before += sum;
                 }
-                if (inc > at && inc - cost(len, plan) <= at) {
+                if (inc > at && inc - cost(len) <= at) {
                     smem[WARPS] = x;
-                    smem[WARPS + 1] = at - (inc - cost(len, plan));
+                    smem[WARPS + 1] = at - (inc - cost(len));
                     smem[WARPS + 2] = len;
                 }
                 if (before > at) break;
@@ -221,38 +250,43 @@ template <bool SPARSE> struct AtWalk {
 
     __device__ __forceinline__ bool next(const spin_kv_config& cfg, const KvAttendArgs& a, const AtPlan& plan, AtSegment& s) {
         if (plan.split) {
+#pragma unroll 1
             while (at < end) {
+#pragma unroll 1
                 for (;;) {
                     if (len_v < 0) len_v = virtual_len<SPARSE>(cfg, a, v);
-                    if (into < cost(len_v, plan)) break;
+                    if (into < cost(len_v)) break;
                     into = 0;
                     len_v = -1;
                     ++v;
                 }
                 s.v = v;
                 s.len = len_v;
-                s.units = (len_v + plan.unit - 1) / plan.unit;
-                s.span = s.units + plan.job_units;
-                s.g = mine / plan.mchunks;
-                s.mc = mine % plan.mchunks;
+                s.units = (len_v + UNIT - 1) / UNIT;
+                s.span = s.units + JOB_UNITS;
+                const int2 y = div_mod(mine, plan.mchunks);
+                s.g = y.x;
+                s.mc = y.y;
                 s.cost0 = at - into;
                 const int64_t take = min(s.span - into, end - at);
-                s.u0 = (int)max((int64_t)0, into - plan.job_units);
-                s.u1 = (int)max((int64_t)0, into + take - plan.job_units);
+                s.u0 = (int)max((int64_t)0, into - JOB_UNITS);
+                s.u1 = (int)max((int64_t)0, into + take - JOB_UNITS);
                 at += take;
                 into += take;
                 if (s.u0 != s.u1) return true;  // else the part ends before the job's first unit
             }
             return false;
         }
-        while (job < (int64_t)plan.n_virtual * plan.per) {
-            s.v = (int)(job / plan.per);
-            s.g = (int)(job % plan.per / plan.mchunks);
-            s.mc = (int)(job % plan.mchunks);
+#pragma unroll 1
+        while (job < plan.n_virtual * plan.per) {
+            const int2 x = div_mod(job, plan.per), y = div_mod(x.y, plan.mchunks);
+            s.v = x.x;
+            s.g = y.x;
+            s.mc = y.y;
             job += gridDim.x;
             s.len = virtual_len<SPARSE>(cfg, a, s.v);
             if (s.len == 0) continue;
-            s.units = (s.len + plan.unit - 1) / plan.unit;
+            s.units = (s.len + UNIT - 1) / UNIT;
             s.u0 = 0;
             s.u1 = s.units;
             return true;
@@ -261,7 +295,7 @@ template <bool SPARSE> struct AtWalk {
     }
 
     __device__ __forceinline__ bool done(const AtPlan& plan) const {
-        return plan.split ? at >= end : job >= (int64_t)plan.n_virtual * plan.per;
+        return plan.split ? at >= end : job >= plan.n_virtual * plan.per;
     }
 
     // Once per segment: who joins the pieces of a job that this CTA begins.
@@ -269,11 +303,7 @@ template <bool SPARSE> struct AtWalk {
         if (!plan.split || s.u0 != 0) return;
         int4 o = make_int4(s.v, mine, rank, 0);
         if (s.u1 < s.units) {  // up to the rank that holds the end of the job's cost
-            const int64_t last = s.cost0 + s.span - 1;
-            int64_t c = last * ranks / total;
-            while (total * (c + 1) / ranks <= last) ++c;
-            while (total * c / ranks > last) --c;
-            o.w = (int)(c - rank) + 1;
+            o.w = (int)(cut.rank_of(s.cost0 + s.span - 1) - rank) + 1;
         }
         if (plan.by_job) plan.owner[(int64_t)s.v * plan.per + mine] = o;
         else if (o.w) plan.owner[blockIdx.x] = o;
