@@ -492,11 +492,37 @@ class KvCache:
         return self.k, self.v, self.k_scale, self.v_scale
 
 
+class CoreAttention:
+    """The attention behind the indexer's top-K, with its per-step device buffers: out
+    [R][rows][n_heads][d], lse [R][rows][n_heads] and the workspace."""
+
+    def __init__(self, cfg: SpinKvConfig, cache: KvCache, rows: int = 1, top_k: int = 0, device="cuda"):
+        self.cfg, self.cache, self.rows = cfg, cache, rows
+        shape = (cfg.n_req, rows, cfg.n_heads, cfg.head_dim)
+        self.out = torch.zeros(shape, dtype=TORCH_DTYPE[cfg.dtype], device=device)
+        self.lse = torch.zeros(shape[:3], dtype=torch.float32, device=device)
+        self.row_slots = torch.zeros(shape[:2], dtype=torch.int32, device=device)
+        self.workspace = kv_workspace(cfg, rows, top_k, device)
+
+    def attend(self, q, block_table, n_slots, topk_idx, status, stream=None):
+        """Every row of request r sees its n_slots[r] slots (the indexer's verifier rows do), or the
+        listed ones of them."""
+        row_slots = n_slots.view(-1, 1)
+        if self.rows > 1:
+            with torch.cuda.stream(stream):
+                self.row_slots.copy_(row_slots.expand(-1, self.rows))
+            row_slots = self.row_slots
+        kv_attend(self.cfg, q, *self.cache.tensors, block_table, row_slots, self.rows, topk_idx, self.out, self.lse,
+                  self.workspace, status, stream)
+
+
 class PagePools:
     """The arrays indexed by page that move with it: contiguous tensors [n_pages, ...] on one
     device.  Keeps them alive; a layer stack lists every layer's."""
 
     def __init__(self, *tensors):
+        if not tensors:
+            raise SpinError(1, "at least one pool")
         self.tensors = tensors
         self.n_pages = tensors[0].shape[0]
         self.device = tensors[0].get_device()
@@ -603,11 +629,13 @@ class StepBuffers:
 
 def run_step(cfg, state: LayerState, buf: StepBuffers, q, w, k_pool, k_scale, n_pages,
              block_table, n_slots, q_pos, step=0, layer=0, rho_override=None, accepted=None,
-             stream=None, hint: Optional[TopkHint] = None, block_age=None):
+             stream=None, hint: Optional[TopkHint] = None, block_age=None,
+             core: Optional[CoreAttention] = None, core_q=None):
     """One decode step of one layer through the C ABI: select -> score -> top-K -> EMA
     (or, with rows > 1, select -> union -> score -> top-K -> deferred commit).  With a
     TopkHint the score kernel collects the temporal top-K's candidates and the hinted top-K
-    replaces the plain one."""
+    replaces the plain one.  With a CoreAttention (of top_k = cfg.top_k) its queries core_q then
+    attend to the top-K slots of its cache, whose pages block_table names too: core.out, core.lse."""
     rows = buf.rows
     union = buf.union if rows > 1 else None
     n_union = buf.n_union if rows > 1 else None
@@ -632,6 +660,8 @@ def run_step(cfg, state: LayerState, buf: StepBuffers, q, w, k_pool, k_scale, n_
         indexer_score_ex(cfg, q, w, k_pool, k_scale, n_pages, block_table, blist, nlist, n_slots,
                          rows, buf.scores, buf.status, hint, stream)
         topk_hinted(cfg, buf.scores, w, blist, nlist, n_slots, rows, buf.topk, hint, buf.status, stream)
+    if core is not None:
+        core.attend(core_q, block_table, n_slots, buf.topk, buf.status, stream)
     if rows == 1 and block_age is not None:
         update_ema_age(cfg, state.V, state.D, state.Vmax, state.warm, buf.scores, blist, nlist,
                        n_slots, q_pos, block_age, step, buf.status, stream)
