@@ -493,7 +493,9 @@ typedef struct spin_kv_config {
  * code inside it does.  Products are exact, and sums, softmax weights' sums and the running
  * maximum are fp32; the weights enter their product with the values as one f16 term for
  * BF16 and F16, as two (22 bits) for F32, and queries as one f16 term scaled by a power of two per
- * row (BF16, F16) or two (F32).
+ * row (BF16, F16) or two (F32).  Value scales are to be at most 2^100 in magnitude, and a row's
+ * within a factor of 2^110 of each other (0 counts as 2^-100): beyond that a weight may overflow,
+ * or small ones be lost from the sum.
  *
  * Checked on the device: n_slots outside [0, max_slots] (BAD_N, the row counts as empty), a
  * list entry outside [-1, n_slots) (BAD_LIST) and a slot whose page is outside [0, n_pages)
@@ -518,14 +520,15 @@ spin_status_t spin_kv_attend(const spin_kv_config* cfg, const void* q, const uin
  *             page's finite new values; 0 if they are all zero)
  *   the page's earlier slots   code <- e4m3(code * s_old / s_new)  (unless s_new = s_old)
  *   the new slots              code  = e4m3(x * (1 / s_new)), infinities saturated, NaN kept
- * (quotients and products rounded to fp32; 0 where s_new < 2^-126) and the scale becomes s_new.  Scales only grow within a page, and a page's content does not
- * depend on what was in it before its slot 0 was written.  With power-of-two scales both are
- * exact up to the e4m3 rounding.  Slots behind the new ones are
- * left as they are.  Requests must not share a page they append to (spin_pages_reserve).
+ * (quotients and products rounded to fp32; 0 where s_new < 2^-126) and the scale becomes s_new.
+ * Scales only grow within a page, and a page's content does not depend on what was in it before
+ * its slot 0 was written.  With power-of-two scales both are exact up to the e4m3 rounding.  Slots
+ * behind the new ones are left as they are.  Requests must not share a page they append to (spin_pages_reserve).
  * max_new: the largest count of new tokens of a request (sizes the launch).
  * Checked on the device: new_start not ascending within [0, n_tokens], a count above max_new,
- * n_before < 0 or past max_slots with the new ones (BAD_N, the request is skipped), a page
- * outside [0, n_pages) (BAD_PAGE, that page is skipped). */
+ * n_before < 0 or past max_slots with the new ones (BAD_N, the request is skipped; where
+ * new_start descends, requests behind that may be skipped too), a page outside [0, n_pages)
+ * (BAD_PAGE, that page is skipped). */
 spin_status_t spin_kv_append(const spin_kv_config* cfg, const void* new_k, const void* new_v,
                              int64_t n_tokens, const int32_t* new_start, int32_t max_new,
                              const int32_t* n_before, uint8_t* k_pool, uint8_t* v_pool,

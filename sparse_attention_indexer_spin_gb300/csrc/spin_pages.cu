@@ -13,6 +13,7 @@ namespace spin {
 
 constexpr int kPgThreads = 256;
 constexpr int kPlanThreads = 1024;
+constexpr int kOwnBlocks = 4;          // blocks of a request that one thread of the plan looks at
 constexpr int kPlanPages = 16;         // neighbouring pages a thread of a plan looks at, at a time
 constexpr int kCopyBytes = 16 * 1024;  // bytes one CTA copies at a time
 
@@ -139,11 +140,41 @@ __device__ __forceinline__ Span span_of(int32_t n, int32_t add, int64_t stride) 
     return s;
 }
 
-// Whether block j needs a fresh page; *old is the page it has (-1: none).
+// Whether a block needs a fresh page; *old is the page it has (-1: none).
 __device__ __forceinline__ bool needs_page(const PageTable& t, int64_t at, int32_t* old) {
-    const int32_t e = t.table[at];
-    *old = e >= 0 && e < t.n_pages ? e : -1;
+    *old = page_of(t.table[at], t);
     return *old < 0 || t.ref[*old] > 1;
+}
+
+// Calls f(r, span, fresh) for every request, with the number of blocks of its span that need a fresh page.
+// A span of more than kOwnBlocks blocks is counted by its whole warp, four blocks a lane at a time
+// (a prompt of 131072 slots: 51 us, 420 us by one thread).  Up to 1024 requests lane l of warp w has
+// request 32 l + w, so that a few long prompts fall to as many warps; above, a warp's requests are
+// neighbours, whose lengths are read together (4096 single tokens: 37 us, 60 us spread out).
+template <typename F>
+__device__ __forceinline__ void each_request(const PageTable& t, const int32_t* n_slots, const int32_t* n_new, F f) {
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    for (int base = 0; base < t.n_req; base += kPlanThreads) {
+        const int r = base + (t.n_req <= kPlanThreads ? 32 * lane + wid : (int)threadIdx.x);
+        Span sp{0, 0, false, false};
+        if (r < t.n_req) sp = span_of(n_slots[r], n_new[r], t.stride);
+        const bool by_warp = sp.j1 - sp.j0 > kOwnBlocks;
+        int fresh = 0;
+        int32_t old;
+        if (!by_warp)
+            for (int64_t j = sp.j0; j < sp.j1; ++j) fresh += needs_page(t, r * t.stride + j, &old);
+        for (uint32_t todo = __ballot_sync(0xffffffffu, by_warp); todo; todo &= todo - 1) {
+            const int from = __ffs(todo) - 1;
+            const int64_t at = (int64_t)__shfl_sync(0xffffffffu, r, from) * t.stride;
+            const int64_t j0 = __shfl_sync(0xffffffffu, sp.j0, from), j1 = __shfl_sync(0xffffffffu, sp.j1, from);
+            int n = 0;
+#pragma unroll 4
+            for (int64_t j = j0 + lane; j < j1; j += 32) n += needs_page(t, at + j, &old);
+            n = __reduce_add_sync(0xffffffffu, n);
+            if (lane == from) fresh = n;
+        }
+        f(r, sp, fresh);
+    }
 }
 
 // The plan, by one CTA: (1) count each request's fresh pages and their prefix, (2) list the
@@ -154,23 +185,19 @@ pages_reserve_kernel(PageTable t, const int32_t* n_slots, const int32_t* n_new, 
     pdl_begin();
     __shared__ int s_scan[33];
     __shared__ int s_given;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31;
     constexpr int kMost = 1 << 30;  // prefix sums saturate here (n_pages <= 2^30)
     int carry = 0, sum;
     if (tid == 0) s_given = 0;
+    each_request(t, n_slots, n_new, [&](int r, const Span& sp, int fresh) {
+        if (r >= t.n_req) return;
+        if (sp.bad) set_status(t.status, SPIN_STATUS_BAD_N);
+        w.prefix[r] = fresh;
+    });
+    __syncthreads();
     for (int base = 0; base < t.n_req; base += kPlanThreads) {
         const int r = base + tid;
-        int need = 0;
-        if (r < t.n_req) {
-            const Span sp = span_of(n_slots[r], n_new[r], t.stride);
-            if (sp.bad) set_status(t.status, SPIN_STATUS_BAD_N);
-            int32_t old;
-            for (int64_t j = sp.j0; j < sp.j1; ++j) {
-                page_of(t.table[r * t.stride + j], t);
-                need += needs_page(t, r * t.stride + j, &old);
-            }
-        }
-        const int pre = block_excl_scan(need, s_scan, &sum);
+        const int pre = block_excl_scan(r < t.n_req ? w.prefix[r] : 0, s_scan, &sum);
         if (r < t.n_req) w.prefix[r] = min(kMost, carry + pre);
         carry = min(kMost, carry + sum);
     }
@@ -185,26 +212,52 @@ pages_reserve_kernel(PageTable t, const int32_t* n_slots, const int32_t* n_new, 
     }
     found = min(found, total);
     __syncthreads();
-    for (int r = tid; r < t.n_req; r += kPlanThreads) {
-        const Span sp = span_of(n_slots[r], n_new[r], t.stride);
-        int need = 0;
-        int32_t old;
-        for (int64_t j = sp.j0; j < sp.j1; ++j) need += needs_page(t, r * t.stride + j, &old);
-        const int64_t first = w.prefix[r];
-        const bool ok = need == 0 || first + need <= found;
-        granted[r] = ok && !sp.bad;
-        if (!ok) set_status(t.status, SPIN_STATUS_NO_PAGES);
-        if (!ok || need == 0) continue;
-        int64_t k = first;
-        for (int64_t j = sp.j0; j < sp.j1; ++j) {
-            if (!needs_page(t, r * t.stride + j, &old)) continue;
-            t.table[r * t.stride + j] = w.dst[k];
-            w.aux[k] = old;
-            w.src[k] = old >= 0 && sp.partial && j == sp.j0 ? old : -1;
-            ++k;
+    each_request(t, n_slots, n_new, [&](int r, const Span& sp, int fresh) {
+        bool serve = false;
+        int k = 0;
+        if (r < t.n_req) {
+            k = w.prefix[r];
+            const bool ok = fresh == 0 || (int64_t)k + fresh <= found;
+            granted[r] = ok && !sp.bad;
+            if (!ok) set_status(t.status, SPIN_STATUS_NO_PAGES);
+            serve = ok && fresh > 0;
+            if (serve) atomicMax(&s_given, k + fresh);
         }
-        atomicMax(&s_given, (int)k);
-    }
+        auto give = [&](int64_t at, const Span& s, int64_t j, int32_t old, int to) {
+            t.table[at + j] = w.dst[to];
+            w.aux[to] = old;
+            w.src[to] = old >= 0 && s.partial && j == s.j0 ? old : -1;
+        };
+        const bool by_warp = serve && sp.j1 - sp.j0 > kOwnBlocks;
+        int32_t old;
+        if (serve && !by_warp)
+            for (int64_t j = sp.j0; j < sp.j1; ++j)
+                if (needs_page(t, r * t.stride + j, &old)) give(r * t.stride, sp, j, old, k++);
+        for (uint32_t todo = __ballot_sync(0xffffffffu, by_warp); todo; todo &= todo - 1) {
+            const int from = __ffs(todo) - 1;
+            const int64_t at = (int64_t)__shfl_sync(0xffffffffu, r, from) * t.stride;
+            Span s;
+            s.j0 = __shfl_sync(0xffffffffu, sp.j0, from);
+            s.j1 = __shfl_sync(0xffffffffu, sp.j1, from);
+            s.partial = __shfl_sync(0xffffffffu, (int)sp.partial, from);
+            int to = __shfl_sync(0xffffffffu, k, from);
+            for (int64_t j4 = s.j0; j4 < s.j1; j4 += 128) {
+                bool needs[4];
+                int32_t olds[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t j = j4 + 32 * i + lane;
+                    needs[i] = j < s.j1 && needs_page(t, at + j, &olds[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t m = __ballot_sync(0xffffffffu, needs[i]);
+                    if (needs[i]) give(at, s, j4 + 32 * i + lane, olds[i], to + __popc(m & ((1u << lane) - 1)));
+                    to += __popc(m);
+                }
+            }
+        }
+    });
     __syncthreads();
     const int given = s_given;
     for (int k = tid; k < given; k += kPlanThreads) {

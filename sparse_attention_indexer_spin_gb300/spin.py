@@ -526,6 +526,8 @@ class PagePools:
         self.tensors = tensors
         self.n_pages = tensors[0].shape[0]
         self.device = tensors[0].get_device()
+        if self.n_pages < 1:
+            raise SpinError(1, "pools without pages")
         for i, t in enumerate(tensors):
             if t.shape[0] != self.n_pages or t.get_device() != self.device or not t.is_contiguous() or not t.is_cuda:
                 raise SpinError(1, "pool %d: contiguous CUDA tensors of as many pages on one device" % i)
@@ -552,8 +554,8 @@ def pages_fork(table_in, parent, table_out, ref, status, stream=None):
     (R, bt), (n_pages,) = table_out.shape, ref.shape
     _check(lib().spin_pages_fork(
         R, n_pages, _arg("table_in", table_in, torch.int32, (R, bt), dev), bt,
-        _arg("parent", parent, torch.int32, (R,), dev), _arg("table_out", table_out, torch.int32, (R, bt), dev), _arg("ref", ref, torch.int32, (n_pages,), dev),
-        _status_arg(status, dev), _stream(stream)))
+        _arg("parent", parent, torch.int32, (R,), dev), _arg("table_out", table_out, torch.int32, (R, bt), dev),
+        _arg("ref", ref, torch.int32, (n_pages,), dev), _status_arg(status, dev), _stream(stream)))
 
 
 def pages_free(block_table, keep_slots, ref, status, stream=None):
@@ -562,8 +564,8 @@ def pages_free(block_table, keep_slots, ref, status, stream=None):
     (R, bt), (n_pages,) = block_table.shape, ref.shape
     _check(lib().spin_pages_free(
         R, n_pages, _arg("block_table", block_table, torch.int32, (R, bt), dev), bt,
-        _arg("keep_slots", keep_slots, torch.int32, (R,), dev), _arg("ref", ref, torch.int32, (n_pages,), dev), _status_arg(status, dev),
-        _stream(stream)))
+        _arg("keep_slots", keep_slots, torch.int32, (R,), dev), _arg("ref", ref, torch.int32, (n_pages,), dev),
+        _status_arg(status, dev), _stream(stream)))
 
 
 def pages_reserve(block_table, n_slots, n_new, ref, pools, granted, workspace, status, stream=None):
@@ -574,8 +576,8 @@ def pages_reserve(block_table, n_slots, n_new, ref, pools, granted, workspace, s
     _check(lib().spin_pages_reserve(
         R, n_pages, _arg("block_table", block_table, torch.int32, (R, bt), dev), bt,
         _arg("n_slots", n_slots, torch.int32, (R,), dev), _arg("n_new", n_new, torch.int32, (R,), dev),
-        _arg("ref", ref, torch.int32, (n_pages,), dev), *_pools_of(pools, n_pages, dev), _arg("granted", granted, torch.int32, (R,), dev),
-        ws, ws_bytes, _status_arg(status, dev), _stream(stream)))
+        _arg("ref", ref, torch.int32, (n_pages,), dev), *_pools_of(pools, n_pages, dev),
+        _arg("granted", granted, torch.int32, (R,), dev), ws, ws_bytes, _status_arg(status, dev), _stream(stream)))
 
 
 def pages_compact(block_table, ref, pools, n_live, workspace, status, stream=None):
@@ -584,9 +586,9 @@ def pages_compact(block_table, ref, pools, n_live, workspace, status, stream=Non
     (R, bt), (n_pages,) = block_table.shape, ref.shape
     ws, ws_bytes = _workspace_arg(workspace, dev)
     _check(lib().spin_pages_compact(
-        R, n_pages, _arg("block_table", block_table, torch.int32, (R, bt), dev), bt, _arg("ref", ref, torch.int32, (n_pages,), dev),
-        *_pools_of(pools, n_pages, dev), _arg("n_live", n_live, torch.int32, (1,), dev), ws, ws_bytes,
-        _status_arg(status, dev), _stream(stream)))
+        R, n_pages, _arg("block_table", block_table, torch.int32, (R, bt), dev), bt,
+        _arg("ref", ref, torch.int32, (n_pages,), dev), *_pools_of(pools, n_pages, dev),
+        _arg("n_live", n_live, torch.int32, (1,), dev), ws, ws_bytes, _status_arg(status, dev), _stream(stream)))
 
 
 # ------------------------------------------------------------------------ convenience

@@ -163,6 +163,30 @@ def test_reserve_edges():
     assert t.tolist() == [[0, 1, 2]] and rf.tolist() == [1, 1, 1, 0] and st == 0
 
 
+@pytest.mark.parametrize("R,spare", [(1, 5), (40, 9000), (40, 100000), (1100, 20000)])
+def test_reserve_long_prompts(R, spare):
+    """Prompts of 3 to 700 blocks beside single tokens, some over blocks that are there already,
+    alone or shared."""
+    rng = np.random.default_rng(R + spare)
+    lens = rng.integers(0, 20000, R) * (rng.random(R) < 0.3)
+    n_pages = int(sum(-(-n // 64) for n in lens)) + spare
+    table, ref = state(rng, lens, n_pages, 1100)
+    parent = np.where(rng.random(R) < 0.6, np.arange(R), rng.integers(-1, R, R))
+    table, ref = o.fork(table, parent, ref)
+    n = np.where(parent >= 0, lens[parent], 0)
+    n = n - rng.integers(0, n + 1) * (rng.random(R) < 0.5)                  # rolled back, far or not at all
+    add = np.where(rng.random(R) < 0.5, rng.integers(0, 3, R), rng.choice([130, 257, 64 * 33, 64 * 128 + 1, 44800], R))
+    if R == 1:
+        n, add = np.array([100]), np.array([64 * 300])
+    pools = make_pools(rng, n_pages, [(8,)])
+    want = o.reserve(table, n, add, ref, pools_w := [p.copy() for p in pools])
+    got = run_reserve(table, ref, n, add, pools)
+    for x, y in zip(got[:3], want):
+        assert np.array_equal(x, y)
+    assert np.array_equal(got[3][0], pools_w[0])
+    assert got[4] == (0 if want[2].all() else B["NO_PAGES"])
+
+
 @pytest.mark.parametrize("n_pages,live", [(1, 0), (1, 1), (5, 2), (64, 64), (1000, 300), (1025, 1024), (5000, 1),
                                           (9000, 6000), (40000, 20000)])
 def test_compact(n_pages, live):
