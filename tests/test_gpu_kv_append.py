@@ -176,3 +176,33 @@ def test_pool_beyond_32_bit_offsets():
     assert np.array_equal(k[at].cpu().numpy(), pk) and np.array_equal(ks[at].cpu().numpy(), sk)
     assert np.array_equal(v[at].cpu().numpy()[pk != 0], (pk ^ 128)[pk != 0]) and np.array_equal(vs[at].cpu().numpy(), sk)
     assert int((k != 0).flatten(1).any(1).sum()) == 2
+
+
+def test_one_prompt_among_many_requests():
+    """Ragged counts of more requests than a CTA looks at in one go, some refused."""
+    rng = np.random.default_rng(9)
+    kvh, d, R = 2, 32, 700
+    count = rng.integers(0, 4, R)
+    count[[3, 255, 256, 640]] = [500, 130, 65, 333]
+    before = rng.integers(0, 200, R)
+    bad = np.array([0, 77, 256, 511, 699])
+    n_pages = int(sum(-(-(b + c) // 64) for b, c in zip(before, count))) + 3
+    table = _kv.make_table(rng, before + count, n_pages)
+    start = np.concatenate([[0], np.cumsum(count)]).astype(np.int32)
+    new = [torch.from_numpy(rng.normal(size=(int(start[-1]), kvh, d))).to(torch.bfloat16) for _ in range(2)]
+    cfg = spin.make_kv_config(R, 64 * table.shape[1], 1, kvh, kvh, d, "bf16")
+    pools = list(_kv.make_pools(rng, n_pages, kvh, d))
+    dv, status = [_kv.dev(x) for x in pools], torch.zeros(1, dtype=torch.int32, device="cuda")
+    given = before.copy()
+    given[bad] = [-1, cfg.max_slots + 1, -5, cfg.max_slots + 1, -2 ** 31]
+    spin.kv_append(cfg, *[x.cuda() for x in new], _kv.dev(start), 500, _kv.dev(given.astype(np.int32)), *dv, _kv.dev(table),
+                   status)
+    assert int(status.item()) == spin.STATUS_BITS["BAD_N"]
+    for r in range(R):
+        if r in bad:
+            continue
+        for i in range(2):
+            o.append(new[i].double().numpy()[start[r]:start[r + 1]], [0, count[r]], before[r:r + 1], pools[i], pools[2 + i],
+                     table[r:r + 1])
+    for x, y in zip(dv, pools):
+        assert np.array_equal(x.cpu().numpy(), y)
