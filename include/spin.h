@@ -19,8 +19,12 @@
  *   (spin_select_blocks with rows > 1) and replays the EMA updates of the accepted
  *   prefix of rows once verification is known (spin_commit_mtp).
  *
+ * Beside the step: the paged 8-bit KV cache its top-K points into, with the attention that
+ * reads it (spin_kv_attend), the append that writes it (spin_kv_append) and the management of
+ * its pages (spin_pages_*).
+ *
  * Conventions (every entry point):
- *   - All pointers except `cfg`, `bytes` and those of the per-layer budget functions
+ *   - All pointers except `cfg`, `bytes`, `pools` and those of the per-layer budget functions
  *     (host functions on host arrays) are DEVICE pointers owned by the caller; the
  *     library allocates nothing and keeps no state between calls (except the built-in
  *     scratch array of spin_select_blocks_noalloc, see there).

@@ -16,6 +16,26 @@
 // value scale costs no precision, and weights lose bits only below 2^-26 of the largest.  The
 // reference moves only when a maximum exceeds it by more than 2^3, which spares most of the
 // rescaling of o.
+//
+// Shape.  A warp takes every fourth tile of 32 slots of its CTA's segment through a ring of its own
+// (two stages of cp.async, no barrier inside a segment), multiplies with mma.sync m16n8k16, and
+// keeps queries, scores, weights and o in registers; the four warps are merged once per segment.
+// The codes have to become f16 in registers anyway, on their way from shared memory to the
+// products, and 16 or 32 query rows fill an m16 tile but an eighth or a quarter of a tcgen05 one:
+// such a kernel (codes converted into shared memory, o in tensor memory) was built and took 511 us
+// where this takes 402, its hand-offs between converting, multiplying and weighting warps alone
+// 3100 cycles a tile of 128 slots.
+//
+// What bounds it (one GB300, D = 128): memory where few query rows share a key head, and then the
+// ends of the launch (its start 2 us, CTAs that end up to a tenth apart, the join 6.5 us); above
+// some 16 rows a key head the products: a scheduler has two warps to choose from, the tensor pipe
+// is active 45 % of the time and conversions take a third of the issue slots.
+//   1 request of 131072 slots, 64 heads on 8:          56 us, 4.8 TB/s (6.7 TB/s a slot more)
+//   64 requests of 100 to 8192 slots, 32 heads on 8:   54 us, 4.5 TB/s
+//   16 of 4096 to 32768, 4 rows of 64 heads on 8, f16: 121 us, 3.8 TB/s
+//   32 of 100000 to 131072, 64 heads on one:           402 us, 2.3 TB/s, 0.3 PFLOP/s
+//   96 requests, 512 listed slots, 64 heads on one:    22 us, list -> page -> code in turn;
+//     2048 listed slots: 53 us, a tile's chain of dependent instructions
 #include "spin_kv_attend.cuh"
 
 namespace spin {
@@ -29,7 +49,8 @@ constexpr int kAtUnit = 64;      // slots in a unit of work
 // the merge of its warps: 4 us beside 1.1 us a unit with the GPU full).
 constexpr int kAtJobUnits = 4;
 // A job is split unless whole jobs cost at most this many units more on the busiest CTA: the
-// joining launch costs about as much.
+// joining launch costs about as much (6.5 us; a unit takes 1.1 us with the GPU full,
+// less where it is not).
 constexpr int kAtSplitGain = 12;
 
 // ------------------------------------------------------------------------ small helpers
@@ -75,6 +96,9 @@ template <int D, bool SPARSE> struct AtStage {  // byte offsets in a stage
     static constexpr int kBytes = kKs + (SPARSE ? 512 : 128);
 };
 
+// CTAs on an SM: three where registers and shared memory allow
+template <int D, int MT, bool SPLIT> constexpr int at_ctas() { return D == 256 ? 1 : MT == 2 || (SPLIT && D == 128) ? 2 : 3; }
+
 template <int D, int MT, bool SPLIT, bool SPARSE> struct AtSmem {
     static constexpr int kRows = 16 * MT;
     static constexpr int kRing = kAtWarps * kAtStages * AtStage<D, SPARSE>::kBytes;
@@ -90,9 +114,6 @@ template <int D> __device__ __forceinline__ int merge_at(int row, int f) {
     if constexpr (D == 64) return (f & ~3) | ((f & 3) ^ (((f >> 3) & 1) + 2 * (row & 1)));
     else return (f & ~7) | ((f & 7) ^ (((f >> 3) & 3) + 4 * (row & 1)));
 }
-
-// CTAs on an SM: three where registers and shared memory allow
-template <int D, int MT, bool SPLIT> constexpr int at_ctas() { return D == 256 ? 1 : MT == 2 || (SPLIT && D == 128) ? 2 : 3; }
 
 // --------------------------------------------------------------------------- the kernel
 template <typename T, int D, int MT, bool SPARSE>
@@ -138,30 +159,29 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
         const int row_n = SPARSE ? row_slots(a, br0, cfg.max_slots) : 0;
         const int64_t row_bytes = (int64_t)kvh * d;
 
-        // Entries and pages are read ahead of the copies that need them: a list entry two tiles, a
-        // page one tile.
-        auto entry = [&](int k) -> int {  // slot of this lane in the warp's k-th tile, -1: none
-            const int t = tile0 + wid + k * kAtWarps;
-            if constexpr (SPARSE) {
-                const int e = t * kAtTile + lane;
-                if (k >= nt || e >= a.top_k) return -1;
-                const int i = a.list[(int64_t)v * a.top_k + e];
-                if (i >= 0 && i < row_n) return i;
-                if (i != -1) set_status(a.status, SPIN_STATUS_BAD_LIST);
-                return -1;
-            } else {
-                const int i = t * kAtTile + lane;
-                return k < nt && i < len ? i : -1;
-            }
+        // Pages are read as many tiles ahead of the copies that need them as the ring holds, list
+        // entries one more; they are looked at when they are needed, not when they are read, so that
+        // nothing waits for them in between.
+        auto entry = [&](int k) -> int {  // slot of this lane in the warp's k-th tile, -1: none; unchecked with a list
+            const int i = (tile0 + wid + k * kAtWarps) * kAtTile + lane;
+            if constexpr (SPARSE) return k < nt && i < a.top_k ? a.list[(int64_t)v * a.top_k + i] : -1;
+            else return k < nt && i < len ? i : -1;
         };
-        auto page_at = [&](int i) -> int {
-            if (i < 0) return -1;
-            const int p = table[i >> 6];
-            if (p >= 0 && p < a.n_pages) return p;
-            set_status(a.status, SPIN_STATUS_BAD_PAGE);
+        auto listed = [&](int i) -> int {
+            if (i >= 0 && i < row_n) return i;
+            if (i != -1) set_status(a.status, SPIN_STATUS_BAD_LIST);
             return -1;
         };
-        int e_now = entry(0), e_next = entry(1), p_now = page_at(e_now);
+        auto page_at = [&](int i) -> int { return i >= 0 ? table[i >> 6] : -1; };  // unchecked
+        int e[SPARSE ? kAtStages + 1 : 1], p[kAtStages];
+        if constexpr (SPARSE) {
+#pragma unroll
+            for (int i = 0; i <= kAtStages; ++i) e[i] = entry(i);
+#pragma unroll
+            for (int i = 0; i < kAtStages; ++i) e[i] = listed(e[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kAtStages; ++i) p[i] = page_at(SPARSE ? e[SPARSE ? i : 0] : entry(i));
 
         constexpr int CH = D / 16;             // 16-byte chunks of a row
         constexpr int RS = 32 / CH;            // rows a warp copies at a time
@@ -172,10 +192,11 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
         auto issue = [&](int k) {  // the k-th tile's copies into its stage
             if (k < nt) {
                 const uint32_t so = (uint32_t)((k % kAtStages) * St::kBytes);
-                const bool live = p_now >= 0;
+                const bool slot = (SPARSE ? e[0] : entry(k)) >= 0, live = slot && p[0] >= 0 && p[0] < a.n_pages;
+                if (slot && !live) set_status(a.status, SPIN_STATUS_BAD_PAGE);
                 const uint32_t mask = __ballot_sync(0xffffffffu, live);
                 if constexpr (SPARSE) {
-                    const int64_t row = live ? (int64_t)p_now * kBlock + (e_now & 63) : 0;
+                    const int64_t row = live ? (int64_t)p[0] * kBlock + (e[0] & 63) : 0;
 #pragma unroll
                     for (int i = 0; i < CH; ++i) {
                         const int from = crow + RS * i;
@@ -184,12 +205,12 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
                         cp16(kdst + so + 512 * i, a.k_pool + (ok ? src : 0), ok);
                         cp16((vdst ^ value_flip<D>(i)) + so + 512 * i, a.v_pool + (ok ? src : 0), ok);
                     }
-                    const int64_t sc = live ? (int64_t)p_now * kvh + g : 0;
+                    const int64_t sc = live ? (int64_t)p[0] * kvh + g : 0;
                     cp4(ring + so + St::kKs + 4 * lane, a.k_scale + sc, live);
                     cp4(ring + so + St::kVs + 4 * lane, a.v_scale + sc, live);
                 } else {
                     // one page: the live slots are the first ones
-                    const int n_live = __popc(mask), page = __shfl_sync(0xffffffffu, p_now, 0);
+                    const int n_live = __popc(mask), page = __shfl_sync(0xffffffffu, p[0], 0);
                     const int first = (tile0 + wid + k * kAtWarps) * kAtTile & (kBlock - 1);
                     const int64_t src = n_live ? ((int64_t)page * kBlock + first) * row_bytes + lane_src : 0;
                     const int64_t step = RS * row_bytes;
@@ -205,9 +226,17 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
                 }
                 if (lane == 0)
                     asm volatile("st.shared.u32 [%0], %1;" ::"r"(ring + so + St::kMask), "r"(mask) : "memory");
-                e_now = e_next;
-                p_now = page_at(e_now);
-                e_next = entry(k + 2);
+#pragma unroll
+                for (int i = 0; i + 1 < kAtStages; ++i) p[i] = p[i + 1];
+                if constexpr (SPARSE) {
+#pragma unroll
+                    for (int i = 0; i < kAtStages; ++i) e[i] = e[i + 1];
+                    e[kAtStages - 1] = listed(e[kAtStages - 1]);
+                    p[kAtStages - 1] = page_at(e[kAtStages - 1]);
+                    e[kAtStages] = entry(k + kAtStages + 1);
+                } else {
+                    p[kAtStages - 1] = page_at(entry(k + kAtStages));
+                }
             }
             cp_commit();
         };
@@ -644,15 +673,25 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
 
 // ------------------------------------------------------------------------------ host side
 static int at_dim(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
-// one row tile (16 query rows of a key/value head) a warp, two where there are more; a 256-wide
-// output leaves registers for one
-static int at_mtiles(int D, int M) { return M > 16 && D <= 128 ? 2 : 1; }
-
 // Two records for every CTA of any variant, 32 rows each at most.
 size_t kv_attend_workspace_bytes(const spin_kv_config& cfg, int, int) {
     const int D = at_dim(cfg.head_dim);
     const size_t G = kAtMostCtas * (size_t)device_sm_count();
     return (G * sizeof(int4) + 255) / 256 * 256 + G * 2 * 32 * (size_t)(D + 2) * sizeof(float);
+}
+
+// units of the longest job; CTAs that the GPU holds; whether jobs are divided
+static int64_t at_units(const spin_kv_config& cfg, const KvAttendArgs& a) {
+    return ((a.list ? a.top_k : cfg.max_slots) + kAtUnit - 1) / kAtUnit;
+}
+template <int D, int MT, bool SPLIT> static int64_t at_room() {
+    const int sms = device_sm_count();
+    return at_ctas<D, MT, SPLIT>() * (int64_t)(sms < kAtMostSms ? sms : kAtMostSms);
+}
+static bool at_split(int64_t jobs, int64_t most, int64_t per, int64_t ctas) {
+    // whole jobs: ceil(jobs / ctas) * most units on the busiest CTA; split: jobs * most / ctas
+    const int64_t ranks = ctas / per;
+    return ranks > 0 && (jobs + ctas - 1) / ctas * most > jobs * most / (ranks * per) + kAtSplitGain;
 }
 
 template <typename T, int D, int MT, bool SPARSE>
@@ -669,12 +708,9 @@ static cudaError_t launch_at(const spin_kv_config& cfg, const KvAttendArgs& a, c
     p.n_virtual = SPARSE ? cfg.n_req * a.rows : cfg.n_req;
     p.per = cfg.kv_heads * p.mchunks;
     p.crows = L::kRows;
-    const int64_t jobs = (int64_t)p.n_virtual * p.per;
-    const int64_t most = ((SPARSE ? a.top_k : cfg.max_slots) + kAtUnit - 1) / kAtUnit;
-    const int64_t ctas = at_ctas<D, MT, SPLIT>() * (int64_t)(device_sm_count() < kAtMostSms ? device_sm_count() : kAtMostSms);
-    // whole jobs: ceil(jobs / ctas) * most units on the busiest CTA; split: jobs * most / ctas
+    const int64_t jobs = (int64_t)p.n_virtual * p.per, most = at_units(cfg, a), ctas = at_room<D, MT, SPLIT>();
     const int64_t ranks = ctas / p.per, most_ranks = p.n_virtual * (most + kAtJobUnits + kAtMinCost - 1) / kAtMinCost;
-    p.split = ranks > 0 && (jobs + ctas - 1) / ctas * most > jobs * most / (ranks * p.per) + kAtSplitGain;
+    p.split = at_split(jobs, most, p.per, ctas);
     const int G = (int)(p.split ? (most_ranks < ranks ? most_ranks : ranks) * p.per : jobs < ctas ? jobs : ctas);
     p.ranks = G / p.per;
     p.by_job = jobs <= G;
@@ -691,13 +727,26 @@ static cudaError_t launch_list(const spin_kv_config& cfg, const KvAttendArgs& a,
     return a.list ? launch_at<T, D, MT, true>(cfg, a, s) : launch_at<T, D, MT, false>(cfg, a, s);
 }
 
+// One row tile (16 query rows of a key/value head) a warp, or two where there are more rows: every
+// converted code then feeds two products (64 heads on one key head 402 us, 527 with one tile; four
+// rows of 64 heads on 8 121 and 154 us), at two CTAs an SM instead of three.  Short whole jobs that
+// are all on the GPU at once take one: a tile is then half the latency (64 requests of 100 to 700
+// slots, 64 heads on one: 16 and 19 us); with lists, whose tiles slow each other more, where each
+// job has an SM to itself (512 slots each: 4 requests 13 and 14.5 us, 96 requests 23.4 and 22 us).
+template <typename T, int D>
+static cudaError_t launch_rows(const spin_kv_config& cfg, const KvAttendArgs& a, cudaStream_t s) {
+    const int64_t rows = a.list ? 1 : a.rows, M = cfg.n_heads / cfg.kv_heads * rows;
+    const int64_t per = cfg.kv_heads * ((M + 15) / 16), jobs = (a.list ? cfg.n_req * (int64_t)a.rows : cfg.n_req) * per;
+    const int64_t ctas = at_room<D, 1, std::is_same<T, float>::value>();
+    if (M <= 16 || (jobs <= (a.list ? device_sm_count() : ctas) && !at_split(jobs, at_units(cfg, a), per, ctas))) return launch_list<T, D, 1>(cfg, a, s);
+    return launch_list<T, D, 2>(cfg, a, s);
+}
+
 template <typename T>
 static cudaError_t launch_typed(const spin_kv_config& cfg, const KvAttendArgs& a, cudaStream_t s) {
-    const int M = cfg.n_heads / cfg.kv_heads * (a.list ? 1 : a.rows), D = at_dim(cfg.head_dim);
-    const int mt = at_mtiles(D, M);
-    if (D == 256) return launch_list<T, 256, 1>(cfg, a, s);
-    if (D == 128) return mt == 1 ? launch_list<T, 128, 1>(cfg, a, s) : launch_list<T, 128, 2>(cfg, a, s);
-    return mt == 1 ? launch_list<T, 64, 1>(cfg, a, s) : launch_list<T, 64, 2>(cfg, a, s);
+    const int D = at_dim(cfg.head_dim);
+    if (D == 256) return launch_list<T, 256, 1>(cfg, a, s);  // (a 256-wide output leaves registers for one tile)
+    return D == 128 ? launch_rows<T, 128>(cfg, a, s) : launch_rows<T, 64>(cfg, a, s);
 }
 
 cudaError_t launch_kv_attend(const spin_kv_config& cfg, const KvAttendArgs& a, cudaStream_t s) {

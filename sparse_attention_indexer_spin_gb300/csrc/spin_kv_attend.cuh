@@ -352,7 +352,8 @@ __device__ __forceinline__ float row_lse(float ref, float l) {
 
 // Joins the pieces of the jobs that were divided: its first rank's second record, then the first
 // records of the ranks after it.  One CTA per job and query row: the pieces' factors first, then
-// each warp adds up every fourth piece.
+// each warp adds up every fourth piece.  A chain of latencies bounds it (launch, owner, factors,
+// pieces): 6.5 us for 64 rows of 57 pieces; a CTA for all rows of a job took 26 us.
 constexpr int kJoinWarps = 4;
 
 template <typename T, int D>

@@ -6,6 +6,11 @@
 // is 0.  There is no free list: fresh pages are the lowest free ones, found by a scan over the
 // counts, so a result depends on the state alone and never on the order of atomics (counts
 // are only added to and subtracted from while other threads may).
+//
+// What bounds it.  Tables and counts are small: a call is a launch and a chain of a few dependent
+// reads, and the plans are one CTA, which needs no other CTA's answer (reserve: 24 us for 256
+// requests of a token, with its copying launch).  Copies run at the memory's rate:
+// 0.44 GB moved in a pool of 1.6 GB, with the release and the plan before it, 155 us.
 #include "spin_common.cuh"
 #include "spin_internal.h"
 

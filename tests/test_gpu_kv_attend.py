@@ -279,3 +279,20 @@ def test_streams_graphs_and_guard_bands():
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(lse, wlse)
     assert (band[:128] == 7).all() and (band[-128:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("heads,kvh,rows,d", [(64, 1, 1, 128), (40, 2, 1, 80), (128, 2, 8, 64), (16, 2, 4, 128)])
+def test_many_query_rows_of_a_key_head_under_a_large_capacity(dtype, heads, kvh, rows, d):
+    """More than 16 query rows a key head, in jobs that are divided and in ones that are whole."""
+    check(dtype, heads, kvh, d, [rows + 63, 66, 2, 0, 700], rows=rows, max_slots=30000, seed=rows)
+    check(dtype, heads, kvh, d, [rows + 63, 66, 2, 0, 700], rows=rows, seed=rows)
+    check(dtype, heads, kvh, d, [1500, 66, 2, 0, 700], rows=rows, top_k=1100, seed=rows)
+    if dtype != "f32":                 # more whole jobs than fit at once
+        check(dtype, heads, kvh, d, [70, 3, 0, 129] * 130, rows=rows, seed=rows)
+
+    def nan(rng, pools, table, n_slots, listed):
+        i = int(n_slots[0, -1]) - 1
+        pools[1][table[0, i // 64], i % 64, 0, 5] = 0x7f
+        _nan_behind(rng, pools, table, n_slots, listed)
+    check(dtype, heads, kvh, d, [700, 64, 10, 0, 65], rows=rows, max_slots=30000, mutate=nan, seed=1)
