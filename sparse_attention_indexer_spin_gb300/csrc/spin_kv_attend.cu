@@ -23,7 +23,7 @@
 // The codes have to become f16 in registers anyway, on their way from shared memory to the
 // products, and 16 or 32 query rows fill an m16 tile but an eighth or a quarter of a tcgen05 one:
 // such a kernel (codes converted into shared memory, o in tensor memory) was built and took 511 us
-// where this takes 402, its hand-offs between converting, multiplying and weighting warps alone
+// where this takes 396, its hand-offs between converting, multiplying and weighting warps alone
 // 3100 cycles a tile of 128 slots.
 //
 // What bounds it (one GB300, D = 128): memory where few query rows share a key head, and then the
@@ -32,8 +32,8 @@
 // is active 45 % of the time and conversions take a third of the issue slots.
 //   1 request of 131072 slots, 64 heads on 8:          56 us, 4.8 TB/s (6.7 TB/s a slot more)
 //   64 requests of 100 to 8192 slots, 32 heads on 8:   54 us, 4.5 TB/s
-//   16 of 4096 to 32768, 4 rows of 64 heads on 8, f16: 121 us, 3.8 TB/s
-//   32 of 100000 to 131072, 64 heads on one:           402 us, 2.3 TB/s, 0.3 PFLOP/s
+//   16 of 4096 to 32768, 4 rows of 64 heads on 8, f16: 119 us, 3.9 TB/s
+//   32 of 100000 to 131072, 64 heads on one:           396 us, 2.4 TB/s, 0.3 PFLOP/s
 //   96 requests, 512 listed slots, 64 heads on one:    22 us, list -> page -> code in turn;
 //     2048 listed slots: 53 us, a tile's chain of dependent instructions
 #include "spin_kv_attend.cuh"
@@ -293,7 +293,7 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
             for (int s = 0; s < KS; ++s) qr[s] = sQ[s * 32 + lane];
         }
         float qs[MT][2];
-        int nlim[MT][2], nmin = 0x7fffffff;
+        int nlim[MT][2], nmin = 0x7fffffff, nseen = 0x7fffffff;  // shortest row; of those that see this segment
 #pragma unroll
         for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -301,8 +301,10 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
                 qs[i][x] = sQs[16 * i + 8 * x + g8];
                 nlim[i][x] = sN[16 * i + 8 * x + g8];
                 nmin = min(nmin, nlim[i][x]);
+                if (nlim[i][x] > kAtUnit * seg.u0) nseen = min(nseen, nlim[i][x]);
             }
         nmin = __reduce_min_sync(0xffffffffu, nmin);
+        nseen = __reduce_min_sync(0xffffffffu, nseen);
 
         float o[MT][NT][4], mx[MT][2], lsum[MT][2];
 #pragma unroll
@@ -522,17 +524,27 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
             }
 
             // A NaN code that some rows see and others do not would reach the others as 0 x NaN: such codes
-            // leave the tile, and the rows that see them are looked for when the segment ends.
-            if (!SPARSE && rows > 1 && slot0 + kAtTile > nmin) {
+            // leave the tile, and the rows that see them are looked for when the segment ends.  (Rows that
+            // see nothing of the segment, the empty ones of a padded batch, drop their sums instead.)
+            if (!SPARSE && rows > 1 && slot0 + kAtTile > nseen) {
                 bool nan = false;
-#pragma unroll 1
-                for (int e = lane; e < kAtTile * D / 4; e += 32) {
-                    uint32_t w;
-                    const uint32_t at = st + St::kValues + 4 * e;
-                    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
-                    const uint32_t m = ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // bytes that are NaN
-                    nan |= m != 0;
-                    if (m) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(w & ~((m >> 7) * 0xffu)) : "memory");
+#pragma unroll 2
+                for (int e = lane; e < kAtTile * D / 16; e += 32) {
+                    const uint32_t at = st + St::kValues + 16 * e;
+                    const uint4 x = lds128(at);
+                    uint32_t w[4] = {x.x, x.y, x.z, x.w}, any = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) any |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
+                    if (any & 0x80808080u) {
+                        nan = true;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t m = ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // bytes that are NaN
+                            w[i] &= ~((m >> 7) * 0xffu);
+                        }
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                                     : "memory");
+                    }
                 }
                 if (nan) *sNan = 1;
                 __syncwarp();
@@ -630,18 +642,20 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
                 const float mw = sM[w * L::kRows + m];
                 const float c = mw == ninf ? 0.0f : ex2(mw - top);
                 const float4 x = reinterpret_cast<const float4*>(sO + (w * L::kRows + m) * D)[merge_at<D>(m, f)];
-                // a warp without a slot of this row has l = 0 and c = 0; one that saw only NaN scores
-                // has l = NaN, which stays
+                // a warp without a slot of this row has l = 0, and sums that may be 0 x NaN; one that
+                // saw only NaN scores has l = NaN, which stays
                 l = fmaf(c, sL[w * L::kRows + m], l);
-                acc.x = fmaf(c, x.x, acc.x);
-                acc.y = fmaf(c, x.y, acc.y);
-                acc.z = fmaf(c, x.z, acc.z);
-                acc.w = fmaf(c, x.w, acc.w);
+                if (mw != ninf) {
+                    acc.x = fmaf(c, x.x, acc.x);
+                    acc.y = fmaf(c, x.y, acc.y);
+                    acc.z = fmaf(c, x.z, acc.z);
+                    acc.w = fmaf(c, x.w, acc.w);
+                }
             }
             if (!SPARSE && *sNan) {
-                // (from the tile on in which the shortest row ends)
+                // (from the tile on in which the shortest row that sees the segment ends)
                 const int64_t br = br0 + (m0 + m) / group;
-                const int last = min(row_slots(a, br, cfg.max_slots), kAtUnit * seg.u1), first = max(nmin & ~(kAtTile - 1), kAtUnit * seg.u0);
+                const int last = min(row_slots(a, br, cfg.max_slots), kAtUnit * seg.u1), first = max(nseen & ~(kAtTile - 1), kAtUnit * seg.u0);
 #pragma unroll 1
                 for (int k = 0; k < 4 && 4 * f + k < d; ++k)
                     if (nan_value(cfg, a, v, g, 4 * f + k, first, last)) nan_bits |= 1u << k;
@@ -728,8 +742,8 @@ static cudaError_t launch_list(const spin_kv_config& cfg, const KvAttendArgs& a,
 }
 
 // One row tile (16 query rows of a key/value head) a warp, or two where there are more rows: every
-// converted code then feeds two products (64 heads on one key head 402 us, 527 with one tile; four
-// rows of 64 heads on 8 121 and 154 us), at two CTAs an SM instead of three.  Short whole jobs that
+// converted code then feeds two products (64 heads on one key head 396 us, 527 with one tile; four
+// rows of 64 heads on 8 119 and 154 us), at two CTAs an SM instead of three.  Short whole jobs that
 // are all on the GPU at once take one: a tile is then half the latency (64 requests of 100 to 700
 // slots, 64 heads on one: 16 and 19 us); with lists, whose tiles slow each other more, where each
 // job has an SM to itself (512 slots each: 4 requests 13 and 14.5 us, 96 requests 23.4 and 22 us).

@@ -296,3 +296,18 @@ def test_many_query_rows_of_a_key_head_under_a_large_capacity(dtype, heads, kvh,
         pools[1][table[0, i // 64], i % 64, 0, 5] = 0x7f
         _nan_behind(rng, pools, table, n_slots, listed)
     check(dtype, heads, kvh, d, [700, 64, 10, 0, 65], rows=rows, max_slots=30000, mutate=nan, seed=1)
+
+
+@pytest.mark.parametrize("heads,kvh,d,max_slots", [(8, 2, 128, None), (8, 2, 64, 60000), (64, 1, 128, 60000), (8, 8, 256, 60000)])
+def test_rows_of_very_different_lengths_and_nan_values(heads, kvh, d, max_slots):
+    """Empty rows of a padded batch, short and long rows of one request, NaN values among the slots
+    that only some of them see."""
+    lens = [3000, 130, 4000]
+    n_slots = np.array([[3000, 0, 100, 1500], [0, 0, 129, 64], [0, 4000, 0, 1]])
+
+    def nan(rng, pools, table, n_slots, listed):
+        for b, i, dim in ((0, 90, 3), (0, 120, 4), (0, 1499, 5), (0, 2999, 6), (1, 100, 7), (2, 1, 8), (2, 2500, 9)):
+            pools[1][table[b, i // 64], i % 64, 0, dim] = 0x7f
+    for dtype in ("bf16", "f32"):
+        check(dtype, heads, kvh, d, lens, rows=4, n_slots=n_slots, max_slots=max_slots, mutate=nan, seed=2)
+        check(dtype, heads, kvh, d, lens, rows=4, n_slots=n_slots, max_slots=max_slots, seed=3)
