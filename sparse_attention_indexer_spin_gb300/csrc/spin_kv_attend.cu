@@ -7,7 +7,7 @@
 //
 // Numbers.  Everything is in base 2: t_i = log2(e) s_i.  A row keeps a reference m and
 //   l = sum_i 2^(t_i - m),   o = sum_i 2^(t_i - m) vs_i vc_i,   out = o / l
-// in fp32.  Codes become f16 exactly.  q is scaled by a power of two per row to just below 2^15
+// in fp32 (l times 2^-20: a value scale of 0 counts as 2^-100 below).  Codes become f16 exactly.  q is scaled by a power of two per row to just below 2^15
 // and rounded to f16: bf16 and f16 values keep every bit unless they are below 2^-29 of the
 // row's largest (f16's subnormals; off by at most 2^-39 of it).  The weights 2^(t_i - m) vs_i
 // are rounded to f16 for their product with the codes (2^-11 each).  fp32 queries and
@@ -377,7 +377,7 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
                 const float lg = scale_log2(v_);
                 __syncwarp();  // every lane has read the mask
                 asm volatile("st.shared.f32 [%0], %1;" ::"r"(st + St::kLv + 4 * lane), "f"(lg) : "memory");
-                asm volatile("st.shared.f32 [%0], %1;" ::"r"(st + St::kIv + 4 * lane), "f"(in_log_range(v_) ? __frcp_rn(v_) : ex2(-lg)) : "memory");
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(st + St::kIv + 4 * lane), "f"(kAtSumUnit * (in_log_range(v_) ? __frcp_rn(v_) : ex2(-lg))) : "memory");
                 __syncwarp();
                 float ks[8];
 #pragma unroll
@@ -410,7 +410,7 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
                 const float ks = __uint_as_float(u), v_ = __uint_as_float(w);
                 odd = !in_log_range(v_);
                 lv[0] = scale_log2(v_);
-                iv[0] = odd ? ex2(-lv[0]) : __frcp_rn(v_);
+                iv[0] = kAtSumUnit * (odd ? ex2(-lv[0]) : __frcp_rn(v_));
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -666,11 +666,7 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
             }
             if (whole) {
                 const int64_t bh = (br0 + (m0 + m) / group) * H + (int64_t)g * group + (m0 + m) % group;
-                const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-                if (l == 0.0f) acc = make_float4(0, 0, 0, 0);
-                if (4 * f < d)
-                    store4(reinterpret_cast<T*>(a.out) + bh * d + 4 * f,
-                           make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+                if (4 * f < d) store4(reinterpret_cast<T*>(a.out) + bh * d + 4 * f, row_out(acc, l));
                 if (a.lse && f == 0) a.lse[bh] = row_lse(top, l);
             } else {
                 reinterpret_cast<float4*>(rec + m * D)[f] = acc;

@@ -18,6 +18,10 @@ namespace spin {
 
 constexpr float kAtTop = 12.0f;  // log2 of the largest weight when the reference is set
 constexpr float kAtSlack = 3.0f; // a maximum may exceed that by this much before the reference moves
+// The weights' sum l is kept times 2^-20.  A slot adds up to 2^(12 + 3) / vs to l, vs >= 2^-100 as the
+// reference counts it: 2^24 slots reach 2^139, times 2^-20 2^119.  The largest weight's slot alone adds 2^12 / vs
+// >= 2^-88, so that l never underflows either.
+constexpr float kAtSumUnit = 9.5367431640625e-7f;
 
 // ------------------------------------------------------------------------ small helpers
 __device__ __forceinline__ float ex2(float x) {
@@ -347,7 +351,15 @@ static __device__ __noinline__ bool nan_value(const spin_kv_config& cfg, const K
 // lse of a row from its reference and sum.
 __device__ __forceinline__ float row_lse(float ref, float l) {
     const float ninf = __uint_as_float(0xff800000u);
-    return l == 0.0f ? ninf : ((ref == ninf ? 0.0f : ref) + log2f(l)) * 0.6931471805599453f;
+    const float lg = l < 1.2676506e30f ? log2f(l * (1.0f / kAtSumUnit)) : log2f(l) + 20.0f;
+    return l == 0.0f ? ninf : ((ref == ninf ? 0.0f : ref) + lg) * 0.6931471805599453f;
+}
+
+// A row's outputs from its sums: o / l (zeros where there is no weight).  1 / l is normal: l <= 2^119.
+__device__ __forceinline__ float4 row_out(const float4 o, float l) {
+    if (l == 0.0f) return make_float4(0, 0, 0, 0);
+    const float inv = __fdiv_rn(1.0f, l);
+    return make_float4(o.x * kAtSumUnit * inv, o.y * kAtSumUnit * inv, o.z * kAtSumUnit * inv, o.w * kAtSumUnit * inv);
 }
 
 // Joins the pieces of the jobs that were divided: its first rank's second record, then the first
@@ -442,7 +454,6 @@ kv_attend_join_kernel(spin_kv_config cfg, KvAttendArgs a, AtPlan plan, int rows)
     for (int i = 0; i < F; ++i) s_acc[wid][lane * F + i] = acc[i];
     __syncthreads();
     const int64_t bh = ((int64_t)job.x * rows + (m0 + m) / group) * H + (int64_t)g * group + (m0 + m) % group;
-    const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
     for (int f = tid; f < d / 4; f += 32 * kJoinWarps) {
         float4 y = make_float4(0, 0, 0, 0);
 #pragma unroll
@@ -450,8 +461,7 @@ kv_attend_join_kernel(spin_kv_config cfg, KvAttendArgs a, AtPlan plan, int rows)
             const float4 x = *reinterpret_cast<const float4*>(&s_acc[w][4 * f]);
             y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
         }
-        if (l == 0.0f) y = make_float4(0, 0, 0, 0);
-        store4(reinterpret_cast<T*>(a.out) + bh * d + 4 * f, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+        store4(reinterpret_cast<T*>(a.out) + bh * d + 4 * f, row_out(y, l));
     }
     if (a.lse && tid == 0) a.lse[bh] = row_lse(top, l);
 }

@@ -311,3 +311,52 @@ def test_rows_of_very_different_lengths_and_nan_values(heads, kvh, d, max_slots)
     for dtype in ("bf16", "f32"):
         check(dtype, heads, kvh, d, lens, rows=4, n_slots=n_slots, max_slots=max_slots, mutate=nan, seed=2)
         check(dtype, heads, kvh, d, lens, rows=4, n_slots=n_slots, max_slots=max_slots, seed=3)
+
+
+def _whole_requests(kvh):
+    """Requests of kvh key heads whose whole jobs fill the GPU once, at three CTAs an SM."""
+    return 3 * torch.cuda.get_device_properties(0).multi_processor_count // kvh
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("vs", [0.0, 2.0 ** -99, 2.0 ** 99])
+@pytest.mark.parametrize("divided", [True, False])
+def test_sums_of_long_rows_at_the_ends_of_the_value_scales(dtype, vs, divided):
+    """131072 slots of equal scores, whose weights' sum stays finite: lse = ln n and out is the values'
+    mean.  Every term and partial sum is a power of two times a whole number below 2^24, so that sums
+    are exact: out is off by the weight's rounding, 1/l and two products; the logarithm's parts are at
+    most 2^7 in magnitude, so each of its roundings is at most 2^-18."""
+    n, kvh, d = 131072, 8, 64
+    R = 1 if divided else _whole_requests(kvh)
+    k, v = (torch.full((4, 64, kvh, d), 0x38, dtype=torch.uint8, device="cuda") for _ in range(2))   # 1.0
+    ks, vsc = torch.ones((4, kvh), device="cuda"), torch.full((4, kvh), vs, device="cuda")
+    table = (torch.arange(n // 64, dtype=torch.int32, device="cuda") % 4).expand(R, -1).contiguous()
+    cfg = spin.make_kv_config(R, n, 1, kvh, kvh, d, dtype, 0.0)
+    q = torch.randn((R, 1, kvh, d), device="cuda").to(_kv.TYPES[dtype])
+    ns = torch.full((R, 1), n, dtype=torch.int32, device="cuda")
+    out, lse = _kv.run_attend(cfg, q, (k, v, ks, vsc), table, ns, 1)
+    assert float((lse.double() - np.log(n)).abs().max()) <= 2.0 ** -16
+    rel = (2.0 ** -21 if dtype == "f32" else 2.0 ** -11) + 2.0 ** -21 + _kv.HALF_STEP[dtype]
+    assert bool(((out.double() - vs).abs() <= rel * vs).all())
+
+
+def test_sums_of_long_lists_of_zero_values():
+    """A list of 16384 slots whose scores rise by 2.5 octaves behind the first 128: the reference
+    does not follow, so that weights are at their largest, and value scales of 0 count for 2^-100."""
+    K, kvh, d, n = 16384, 8, 64, 8192
+    R = _whole_requests(kvh)
+    k, v = (torch.full((2, 64, kvh, d), 0x38, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks = torch.tensor([[1.0], [1.5]], device="cuda").expand(2, kvh).contiguous()
+    table = torch.ones((R, n // 64), dtype=torch.int32, device="cuda")
+    table[:, 0] = 0
+    listed = torch.full((R, 1, K), 64, dtype=torch.int32, device="cuda")
+    listed[:, :, :128] = 5
+    s = 5 * np.log(2)
+    cfg = spin.make_kv_config(R, n, 1, kvh, kvh, d, "bf16", s / d)
+    q = torch.ones((R, 1, kvh, d), dtype=torch.bfloat16, device="cuda")
+    ns = torch.full((R, 1), n, dtype=torch.int32, device="cuda")
+    out, lse = _kv.run_attend(cfg, q, (k, v, ks, torch.zeros_like(ks)), table, ns, 1, listed)
+    want = np.log(128 * np.exp(s) + (K - 128) * np.exp(1.5 * s))
+    # parts of at most 2^7 with roundings of 2^-18, and sums of 4096 rounded 2^-24 each
+    assert float((lse.double() - want).abs().max()) <= 2.0 ** -16 + 4096 * 2.0 ** -24
+    assert not bool(out.any())
