@@ -15,7 +15,9 @@
 // that the largest weights, value scale included, sit between 2^12 and 2^15: a page's small
 // value scale costs no precision, and weights lose bits only below 2^-26 of the largest.  The
 // reference moves only when a maximum exceeds it by more than 2^3, which spares most of the
-// rescaling of o.
+// rescaling of o.  From 2^20 on an exponent's roundings come near 2^0 (they are at most four of 2^-4 there),
+// and weights would leave f16's range, or all of a row's vanish: such tiles round t_i as the maximum was
+// rounded and keep it at 15 above the reference at most.
 //
 // Shape.  A warp takes every fourth tile of 32 slots of its CTA's segment through a ring of its own
 // (two stages of cp.async, no barrier inside a segment), multiplies with mma.sync m16n8k16, and
@@ -315,6 +317,7 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
             for (int n = 0; n < NT; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.0f;
         }
 
+        bool far = false;   // a reference of kAtFar or more
         for (int k = 0; k < nt; ++k) {
             cp_wait<kAtStages - 1>();
             __syncwarp();
@@ -459,6 +462,7 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
                         const float now = fmaxf(mx[i][r], top[i][r]);
                         const float f = now == ninf ? 1.0f : ex2(mx[i][r] - now);
                         mx[i][r] = now;
+                        far |= now != ninf && fabsf(now) >= kAtFar;
                         lsum[i][r] *= f;
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
@@ -466,13 +470,31 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
                             o[i][n][2 * r + 1] *= f;
                         }
                     }
+                far = __any_sync(0xffffffffu, far);
+            }
+            if (far) {  // the exponents, rounded as the maximum was and bounded
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float m = mx[i][r] == ninf ? 0.0f : mx[i][r];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int x = 2 * r; x < 2 * r + 2; ++x) {
+                                const float y = SPARSE ? s[i][j][x] : __fadd_rn(__fmul_rn(s[i][j][x], c[i][r]), lv[0]);
+                                const float e = __fsub_rn(y, m);
+                                s[i][j][x] = e > kAtTop + kAtSlack ? kAtTop + kAtSlack : e;  // (NaN stays)
+                            }
+                        c[i][r] = 1.0f;
+                    }
             }
             uint4 pw[MT][SPLIT ? 2 : 1][2];
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
                 float bias[2], add[2] = {0.0f, 0.0f};
 #pragma unroll
-                for (int r = 0; r < 2; ++r) bias[r] = (SPARSE ? 0.0f : lv[0]) - (mx[i][r] == ninf ? 0.0f : mx[i][r]);
+                for (int r = 0; r < 2; ++r) bias[r] = far ? 0.0f : (SPARSE ? 0.0f : lv[0]) - (mx[i][r] == ninf ? 0.0f : mx[i][r]);
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll

@@ -18,6 +18,7 @@ namespace spin {
 
 constexpr float kAtTop = 12.0f;  // log2 of the largest weight when the reference is set
 constexpr float kAtSlack = 3.0f; // a maximum may exceed that by this much before the reference moves
+constexpr float kAtFar = 1048576.0f;  // references from here on take care of the exponents' roundings
 // The weights' sum l is kept times 2^-20.  A slot adds up to 2^(12 + 3) / vs to l, vs >= 2^-100 as the
 // reference counts it: 2^24 slots reach 2^139, times 2^-20 2^119.  The largest weight's slot alone adds 2^12 / vs
 // >= 2^-88, so that l never underflows either.

@@ -360,3 +360,42 @@ def test_sums_of_long_lists_of_zero_values():
     # parts of at most 2^7 with roundings of 2^-18, and sums of 4096 rounded 2^-24 each
     assert float((lse.double() - want).abs().max()) <= 2.0 ** -16 + 4096 * 2.0 ** -24
     assert not bool(out.any())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("exponent", [10, 12, 14, 15, 16, 18, 20, 24, 30, 60, 90])
+@pytest.mark.parametrize("form", ["dense", "list", "rows", "divided"])
+def test_scores_far_from_zero(dtype, exponent, form):
+    """Scores of 2^16 to 2^98 that differ by 2^14 and more: one slot takes all of the weight, so that
+    out is its value but for the roundings of a weight, 1/l and two products, and lse its score, off by
+    at most eight roundings of 2^-24."""
+    rng = np.random.default_rng(exponent)
+    heads, kvh, d, n = 8, 2, 64, 700
+    rows = 3 if form == "rows" else 1
+    for sign in (1, -1):
+        pools = list(_kv.make_pools(rng, 14, kvh, d))
+        pools[0][:] = 0
+        pools[0][..., 3] = o.e4m3_encode(rng.choice(np.arange(64, 192, 16), (14, 64, kvh)))
+        pools[2][:] = 1.0
+        table = _kv.make_table(rng, [n], 14, 2000 if form == "divided" else None)
+        for g, i in enumerate(rng.integers(0, n - 2, kvh)):      # the largest score of each head
+            pools[0][table[0, i // 64], i % 64, g, 3] = o.e4m3_encode([192.0 if sign > 0 else 48.0])[0]
+        q = np.zeros((1, rows, heads, d))
+        q[..., 3] = sign * 2.0 ** exponent
+        q = torch.from_numpy(q).to(_kv.TYPES[dtype])
+        cfg = spin.make_kv_config(1, 64 * table.shape[1], rows, heads, kvh, d, dtype, 1.0)
+        listed = rng.permutation(n).astype(np.int32).reshape(1, 1, n) if form == "list" else None
+        ns = (n - np.arange(rows - 1, -1, -1, dtype=np.int32))[None]
+        out, lse = _kv.run_attend(cfg, q.cuda(), [_kv.dev(x) for x in pools], _kv.dev(table), _kv.dev(ns), rows,
+                                  None if listed is None else _kv.dev(listed))
+        ref, rlse, _ = o.attend(q.double().numpy(), *pools, table, ns, 1.0, listed)
+        rel = (2.0 ** -21 if dtype == "f32" else 2.0 ** -11) + 2.0 ** -21 + _kv.HALF_STEP[dtype]
+        assert (np.abs(out.double().cpu().numpy() - ref) <= rel * np.abs(ref)).all()
+        assert (np.abs(lse.double().cpu().numpy() - rlse) <= 2.0 ** -21 * np.abs(rlse)).all()
+
+
+def test_nan_scores_far_from_zero_stay_nan():
+    """A NaN key among scores of 2^30."""
+    def nan(rng, pools, table, n_slots, listed):
+        pools[0][table[0, 1], 3, 1, 7] = 0x7f
+    check("bf16", 8, 2, 64, [130], mutate=nan, q_size=2.0 ** 30, scale=1.0, seed=1)
