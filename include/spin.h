@@ -493,8 +493,8 @@ typedef struct spin_kv_config {
  *   out     = sum_i exp(s_i) v_scale code_v(i) / sum_i exp(s_i)      (over the set)
  *   lse     = ln sum_i exp(s_i)
  * A row with an empty set gets out = 0 and lse = -inf.  A slot listed twice counts twice.
- * Cached values outside a row's set (NaN codes among them) do not reach its outputs; a NaN
- * code inside it does.  Products are exact, and sums, softmax weights' sums and the running
+ * Cached values outside a row's set (NaN codes, and scales of pages that it sees nothing of, among
+ * them) do not reach its outputs; a NaN code inside it does.  Products are exact, and sums, softmax weights' sums and the running
  * maximum are fp32; the weights enter their product with the values as one f16 term for
  * BF16 and F16, as two (22 bits) for F32, and queries as one f16 term scaled by a power of two per
  * row (BF16, F16) or two (F32).  Value scales are to be at most 2^100 in magnitude, and a row's

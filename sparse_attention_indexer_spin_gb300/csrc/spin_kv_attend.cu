@@ -507,22 +507,26 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
 #pragma unroll
                 for (int r = 0; r < 2; ++r) lsum[i][r] = SPARSE ? lsum[i][r] + add[r] : fmaf(add[r], iv[0], lsum[i][r]);
             }
-            if (odd) {  // zero, negative, tiny, huge or NaN: the ratio of scale and power of two
+            if (odd) {  // zero, negative, tiny, huge or NaN: the ratio of scale and power of two, for the
+                        // slots that a row sees (0 x inf and 0 x NaN would reach the others)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
+                        const int at_slot = 8 * j + 2 * t4 + x;
                         uint32_t u;
                         asm volatile("ld.shared.u32 %0, [%1];"
                                      : "=r"(u)
-                                     : "r"(st + St::kVs + (SPARSE ? 4 * (8 * j + 2 * t4 + x) : 0))
+                                     : "r"(st + St::kVs + (SPARSE ? 4 * at_slot : 0))
                                      : "memory");
                         const float v_ = __uint_as_float(u), f = in_log_range(v_) ? 1.0f : v_ * ex2(-scale_log2(v_));
 #pragma unroll
-                        for (int i = 0; i < MT; ++i) {
-                            s[i][j][x] *= f;
-                            s[i][j][2 + x] *= f;
-                        }
+                        for (int i = 0; i < MT; ++i)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                const bool ok = !border || (((mask >> at_slot) & 1u) && (SPARSE || slot0 + at_slot < nlim[i][r]));
+                                s[i][j][2 * r + x] *= ok ? f : 0.0f;
+                            }
                     }
             }
 #pragma unroll

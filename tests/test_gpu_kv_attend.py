@@ -399,3 +399,25 @@ def test_nan_scores_far_from_zero_stay_nan():
     def nan(rng, pools, table, n_slots, listed):
         pools[0][table[0, 1], 3, 1, 7] = 0x7f
     check("bf16", 8, 2, 64, [130], mutate=nan, q_size=2.0 ** 30, scale=1.0, seed=1)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("heads,kvh,rows,d,max_slots", [(8, 2, 2, 64, 700), (64, 1, 4, 128, 700), (16, 2, 3, 256, 700),
+                                                        (8, 2, 4, 128, 60000)])
+def test_value_scales_that_are_not_finite_stay_with_the_rows_that_see_them(bad, dtype, heads, kvh, rows, d, max_slots):
+    """A page that every verifier row but the first sees: the first row's bits, and another request's,
+    do not depend on its value scale."""
+    rng = np.random.default_rng(1)
+    pools = list(_kv.make_pools(rng, 16, kvh, d))
+    table = _kv.make_table(rng, [128 + rows - 1, 700], 16, -(-max_slots // 64))
+    n = np.array([[128 + r for r in range(rows)], [700] * rows], np.int32)
+    q = torch.from_numpy(rng.normal(size=(2, rows, heads, d))).to(_kv.TYPES[dtype]).cuda()
+    cfg = spin.make_kv_config(2, max_slots, rows, heads, kvh, d, dtype)
+    got = []
+    for x in (0.01, bad):
+        pools[3][table[0, 2]] = x
+        got.append(_kv.run_attend(cfg, q, [_kv.dev(p) for p in pools], _kv.dev(table), _kv.dev(n), rows))
+    for clean, other in zip(*got):
+        assert torch.equal(clean[0, 0], other[0, 0]) and torch.equal(clean[1], other[1])
+    assert not bool(got[1][0][0, 1:].isfinite().any())
