@@ -107,7 +107,8 @@ template <int D, int MT, bool SPLIT, bool SPARSE> struct AtSmem {
     static constexpr int kMerge = kAtWarps * kRows * D * 4;          // shares the ring's memory
     static constexpr int kMain = kRing > kMerge ? kRing : kMerge;
     static constexpr int kQ = MT * (SPLIT ? 2 : 1) * (D / 16) * 512;  // query fragments
-    static constexpr int kBytes = kMain + kQ + kRows * 8 + 2 * kAtWarps * kRows * 4 + 128;
+    static constexpr int kNan = SPARSE ? 0 : D * 4;                   // first NaN taken out, of each dimension
+    static constexpr int kBytes = kMain + kQ + kRows * 8 + 2 * kAtWarps * kRows * 4 + 128 + kNan;
 };
 
 // Merged rows in shared memory: float4 f of a row is kept at f ^ rot, so that the eight lanes of
@@ -135,13 +136,12 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
     float* sM = reinterpret_cast<float*>(sN + L::kRows);
     float* sL = sM + kAtWarps * L::kRows;
     int64_t* sScan = reinterpret_cast<int64_t*>(sL + kAtWarps * L::kRows);
-    volatile int* sNan = reinterpret_cast<volatile int*>(sScan + 15);  // a NaN that only some rows see
+    int* sNan = reinterpret_cast<int*>(sScan + 16);  // per dimension, the first slot of a NaN that only some rows see
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
     const int H = cfg.n_heads, kvh = cfg.kv_heads, d = cfg.head_dim, group = H / kvh;
     const int rows = SPARSE ? 1 : a.rows, M = group * rows;
     const float ninf = __uint_as_float(0xff800000u);
 
-    if (tid == 0) *sNan = 0;
     using Walk = AtWalk<SPARSE, kAtUnit, kAtJobUnits>;
     Walk walk;
     walk.template start<kAtWarps>(cfg, a, plan, sScan);
@@ -244,6 +244,9 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
         };
 #pragma unroll 1
         for (int k = 0; k < kAtStages; ++k) issue(k);
+
+        if (!SPARSE && rows > 1)
+            for (int i = tid; i < D; i += kAtThreads) sNan[i] = 0x7fffffff;
 
         // ---- queries: row m is (row m / group, head g * group + m % group), scaled by a power
         // of two and rounded to f16, laid out as the fragments read them
@@ -550,29 +553,30 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
             }
 
             // A NaN code that some rows see and others do not would reach the others as 0 x NaN: such codes
-            // leave the tile, and the rows that see them are looked for when the segment ends.  (Rows that
-            // see nothing of the segment, the empty ones of a padded batch, drop their sums instead.)
+            // leave the tile, and the first one's slot of each dimension is kept: a row sees a NaN of
+            // that dimension if its slots reach so far.  (Rows that see nothing of the segment, the empty
+            // ones of a padded batch, drop their sums instead.)
             if (!SPARSE && rows > 1 && slot0 + kAtTile > nseen) {
-                bool nan = false;
 #pragma unroll 2
-                for (int e = lane; e < kAtTile * D / 16; e += 32) {
-                    const uint32_t at = st + St::kValues + 16 * e;
+                for (int e = lane; e < kAtTile * CH; e += 32) {
+                    const int row = e / CH, ch = e % CH;
+                    const uint32_t at = st + St::kValues + value_at<D>(row, ch);
                     const uint4 x = lds128(at);
                     uint32_t w[4] = {x.x, x.y, x.z, x.w}, any = 0;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) any |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
                     if (any & 0x80808080u) {
-                        nan = true;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint32_t m = ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // bytes that are NaN
                             w[i] &= ~((m >> 7) * 0xffu);
+#pragma unroll 1
+                            for (uint32_t y = m; y; y &= y - 1) atomicMin(sNan + 16 * ch + 4 * i + ((__ffs(y) - 1) >> 3), slot0 + row);
                         }
                         asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                                      : "memory");
                     }
                 }
-                if (nan) *sNan = 1;
                 __syncwarp();
             }
 
@@ -662,7 +666,6 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
             for (int w = 0; w < kAtWarps; ++w) top = fmaxf(top, sM[w * L::kRows + m]);
             float l = 0.0f;
             float4 acc = make_float4(0, 0, 0, 0);
-            uint32_t nan_bits = 0;
 #pragma unroll
             for (int w = 0; w < kAtWarps; ++w) {
                 const float mw = sM[w * L::kRows + m];
@@ -678,17 +681,13 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
                     acc.w = fmaf(c, x.w, acc.w);
                 }
             }
-            if (!SPARSE && *sNan) {
-                // (from the tile on in which the shortest row that sees the segment ends)
-                const int64_t br = br0 + (m0 + m) / group;
-                const int last = min(row_slots(a, br, cfg.max_slots), kAtUnit * seg.u1), first = max(nseen & ~(kAtTile - 1), kAtUnit * seg.u0);
-#pragma unroll 1
-                for (int k = 0; k < 4 && 4 * f + k < d; ++k)
-                    if (nan_value(cfg, a, v, g, 4 * f + k, first, last)) nan_bits |= 1u << k;
-                if (nan_bits & 1u) acc.x = __uint_as_float(0x7fffffffu);
-                if (nan_bits & 2u) acc.y = __uint_as_float(0x7fffffffu);
-                if (nan_bits & 4u) acc.z = __uint_as_float(0x7fffffffu);
-                if (nan_bits & 8u) acc.w = __uint_as_float(0x7fffffffu);
+            if (!SPARSE && rows > 1) {
+                const int n = sN[m];
+                const int4 first = reinterpret_cast<const int4*>(sNan)[f];
+                if (first.x < n) acc.x = __uint_as_float(0x7fffffffu);
+                if (first.y < n) acc.y = __uint_as_float(0x7fffffffu);
+                if (first.z < n) acc.z = __uint_as_float(0x7fffffffu);
+                if (first.w < n) acc.w = __uint_as_float(0x7fffffffu);
             }
             if (whole) {
                 const int64_t bh = (br0 + (m0 + m) / group) * H + (int64_t)g * group + (m0 + m) % group;

@@ -337,18 +337,6 @@ __device__ __noinline__ void write_empty(const spin_kv_config& cfg, const KvAtte
     }
 }
 
-// Whether a NaN value of dimension `dim` is among slots [first, last) of request b: the rare look
-// behind a NaN that only some of a job's rows see.
-static __device__ __noinline__ bool nan_value(const spin_kv_config& cfg, const KvAttendArgs& a, int64_t b, int g, int dim,
-                                              int first, int last) {
-    for (int s = first; s < last; ++s) {
-        const int p = a.block_table[b * a.bt_stride + (s >> 6)];
-        if (p < 0 || p >= a.n_pages) continue;
-        if ((a.v_pool[(((int64_t)p * kBlock + (s & 63)) * cfg.kv_heads + g) * cfg.head_dim + dim] & 0x7f) == 0x7f) return true;
-    }
-    return false;
-}
-
 // lse of a row from its reference and sum.
 __device__ __forceinline__ float row_lse(float ref, float l) {
     const float ninf = __uint_as_float(0xff800000u);

@@ -421,3 +421,31 @@ def test_value_scales_that_are_not_finite_stay_with_the_rows_that_see_them(bad, 
     for clean, other in zip(*got):
         assert torch.equal(clean[0, 0], other[0, 0]) and torch.equal(clean[1], other[1])
     assert not bool(got[1][0][0, 1:].isfinite().any())
+
+
+def test_a_nan_value_does_not_slow_the_call_down():
+    """Rows of 100 and 16384 slots with one NaN value that only the long ones see: found while its tile is
+    at hand, without a second look at the cache."""
+    rng = np.random.default_rng(1)
+    kvh, heads, d, R, n = 2, 16, 128, 4, 16384
+    ns = _kv.dev(np.tile(np.array([100, n, 0, n], np.int32), (R, 1)))
+    pools = list(_kv.make_pools(rng, R * n // 64, kvh, d))
+    table = _kv.make_table(rng, [n] * R, R * n // 64)
+    cfg = spin.make_kv_config(R, n, 4, heads, kvh, d, "bf16")
+    q = torch.from_numpy(rng.normal(size=(R, 4, heads, d))).to(torch.bfloat16).cuda()
+    ws, out, dt, times = spin.kv_workspace(cfg, 4), torch.empty_like(q), _kv.dev(table), []
+    for nan in (False, True):
+        if nan:
+            pools[1][table[0, 1], 50, 0, 5] = 0x7f
+        dv, best = [_kv.dev(p) for p in pools], float("inf")
+        for _ in range(8):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            spin.kv_attend(cfg, q, *dv, dt, ns, 4, None, out, None, ws, None)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        times.append(best)
+    got = out.isnan().cpu().numpy()
+    assert got.sum() == 2 * heads // kvh and got[0, 1, :heads // kvh, 5].all() and got[0, 3, :heads // kvh, 5].all()
+    assert times[1] <= 2 * times[0] + 0.05, times
