@@ -524,7 +524,9 @@ spin_status_t spin_kv_attend(const spin_kv_config* cfg, const void* q, const uin
  *             page's finite new values; 0 if they are all zero)
  *   the page's earlier slots   code <- e4m3(code * s_old / s_new)  (unless s_new = s_old)
  *   the new slots              code  = e4m3(x * (1 / s_new)), infinities saturated, NaN kept
- * (quotients and products rounded to fp32; 0 where s_new < 2^-126) and the scale becomes s_new.
+ * (quotients and products rounded to fp32) and the scale becomes s_new.  s_new < 2^-126 only where the
+ * new values are zeros, infinities and NaN: their codes are +-0, +-448 and NaN then too (infinities
+ * beside nothing finite but zeros thus count as 0, the scale being 0).
  * Scales only grow within a page, and a page's content does not depend on what was in it before
  * its slot 0 was written.  With power-of-two scales both are exact up to the e4m3 rounding.  Slots
  * behind the new ones are left as they are.  Requests must not share a page they append to (spin_pages_reserve).

@@ -101,7 +101,9 @@ def append(x, start, before, pool, scale, table):
                     pool[page, :at, h] = e4m3_encode(c)
                 inv = f32(1) / f32(s) if s >= 2.0 ** -126 else f32(0)
                 with np.errstate(invalid="ignore", over="ignore"):
-                    pool[page, at:at + m, h] = e4m3_encode(new.astype(f32) * inv)
+                    quotient = new.astype(f32) * inv
+                # an infinity stays one, whatever the scale, and saturates
+                pool[page, at:at + m, h] = e4m3_encode(np.where(np.isinf(new), new, quotient))
                 scale[page, h] = s
             t += m
 

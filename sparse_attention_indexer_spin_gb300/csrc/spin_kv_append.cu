@@ -208,7 +208,8 @@ kv_append_kernel(spin_kv_config cfg, KvAppendArgs a, int each) {
 #pragma unroll
         for (int w = 1; w < THREADS / 32; ++w) amax = fmaxf(amax, s_amax[p][w]);
         const float s_new = fmaxf(old[p], pow2_scale(amax));
-        const float inv = s_new >= __uint_as_float(0x00800000u) ? __fdiv_rn(1.0f, s_new) : 0.0f;
+        // (below 2^-126 there are only zeros, infinities and NaN: they keep their codes under any factor but 0)
+        const float inv = s_new >= __uint_as_float(0x00800000u) ? __fdiv_rn(1.0f, s_new) : 1.0f;
         uint8_t* dst = (kv0 + p ? a.pool[1] : a.pool[0]) + (page * kBlock * kvh + h) * d;
         if (tid == 0) (kv0 + p ? a.scale[1] : a.scale[0])[page * kvh + h] = s_new;
         int row = row0, col = col0;

@@ -206,3 +206,42 @@ def test_one_prompt_among_many_requests():
                      table[r:r + 1])
     for x, y in zip(dv, pools):
         assert np.array_equal(x.cpu().numpy(), y)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("d", [32, 128, 256])
+def test_infinities_beside_nothing_finite(dtype, d):
+    """A head whose new values are infinities, NaN and zeros: codes of 448 and NaN under a scale of 0, which
+    the page's next finite values turn into zeros (and NaN)."""
+    kvh, inf = 2, float("inf")
+    cfg = spin.make_kv_config(1, 64, 1, kvh, kvh, d, dtype)
+    c, table = spin.KvCache(1, kvh, d), _kv.dev(np.zeros((1, 1), np.int32))
+
+    def put(x, at):
+        x = x.to(_kv.TYPES[dtype]).cuda()
+        spin.kv_append(cfg, x, -x, _kv.dev(np.array([0, 1], np.int32)), 1, _kv.dev(np.array([at], np.int32)), *c.tensors,
+                       table, None)
+
+    x = torch.zeros((1, kvh, d))
+    x[0, 0, 3], x[0, 0, 5], x[0, 1, :] = inf, float("nan"), -inf
+    put(x, 0)
+    want = torch.zeros((kvh, d), dtype=torch.uint8)
+    want[0, 3], want[1, :] = 0x7e, 0xfe
+    for pool, flip in ((c.k, 0), (c.v, 0x80)):
+        got = pool[0, 0].cpu()
+        assert int(got[0, 5]) & 0x7f == 0x7f
+        got[0, 5] = want[0, 5] ^ flip
+        assert torch.equal(got ^ flip, want)
+    assert not bool(c.k_scale.any()) and not bool(c.v_scale.any())
+    put(torch.ones((1, kvh, d)), 1)
+    assert bool((c.k_scale == 2.0 ** -8).all())
+    old = c.k[0, 0].cpu() & 0x7f
+    assert int(old[0, 5]) == 0x7f and int((old != 0).sum()) == 1
+
+    def mixed(rng, new, pools):
+        for x in new:
+            x[:] = 0.0
+            x[0, 0, 3], x[0, 1, :], x[2, 0, 5], x[3, 1, 6] = inf, -inf, float("nan"), inf
+        for i in (0, 1):
+            pools[2 + i][:] = 0.0
+    check(dtype, 2, d, [0, 64, 5], [1, 1, 2], mutate=mixed)

@@ -219,3 +219,14 @@ def test_oracle_attention_by_hand():
     assert np.allclose(out, 4.0)
     out, lse, _ = o.attend(q, k, v, ks, vs, np.array([[1]]), np.array([[0]]), 0.25)
     assert (out == 0).all() and np.isneginf(lse).all()
+
+
+def test_oracle_appends_infinities_beside_nothing_finite():
+    """Saturated under a scale of 0, and gone with the page's next finite value."""
+    pool, scale = np.zeros((1, 64, 1, 16), np.uint8), np.zeros((1, 1), np.float32)
+    x = np.zeros((1, 1, 16))
+    x[0, 0, :3] = np.inf, -np.inf, np.nan
+    o.append(x, [0, 1], [0], pool, scale, np.zeros((1, 1), np.int32))
+    assert pool[0, 0, 0].tolist() == [126, 254, 127] + [0] * 13 and scale[0, 0] == 0
+    o.append(np.ones((1, 1, 16)), [0, 1], [1], pool, scale, np.zeros((1, 1), np.int32))
+    assert (pool[0, 0, 0] & 127).tolist() == [0, 0, 127] + [0] * 13 and scale[0, 0] == 2.0 ** -8
