@@ -242,11 +242,11 @@ kv_append_kernel(spin_kv_config cfg, KvAppendArgs a, int each) {
 
 template <typename T>
 static cudaError_t launch_typed(const spin_kv_config& cfg, const KvAppendArgs& a, cudaStream_t s) {
-    if (a.max_new == 0) return cudaSuccess;
     // pages touched, at most: n slots touch (n + 62) / 64 + 1, one page more than they fill.  Every
     // request gets as many CTAs as the longest may need where that is no more than all can touch (a
-    // token or so each, or prompts of one length); else a CTA looks its page up (512
-    // requests of 4 tokens: 34 us without, 43 us with the look-up; 64 of 1 token: 11 us both).
+    // token or so each, or prompts of one length; one, which checks the counts, where max_new is 0); else
+    // a CTA looks its page up (512 requests of 4 tokens: 34 us without, 43 us with the look-up; 64 of 1
+    // token: 11 us both).
     int64_t each = ((int64_t)a.max_new + kBlock - 2) / kBlock + 1;
     int64_t pages = a.n_tokens / kBlock + 2 * (int64_t)cfg.n_req;
     if (each * cfg.n_req <= pages) pages = each * cfg.n_req;

@@ -245,3 +245,25 @@ def test_infinities_beside_nothing_finite(dtype, d):
         for i in (0, 1):
             pools[2 + i][:] = 0.0
     check(dtype, 2, d, [0, 64, 5], [1, 1, 2], mutate=mixed)
+
+
+def test_counts_are_checked_where_max_new_is_zero():
+    """Counts above a max_new of 0, and bad places, are reported and nothing is written."""
+    kvh, d = 2, 32
+    cfg = spin.make_kv_config(3, 128, 1, kvh, kvh, d, "f32")
+    new = torch.randn((8, kvh, d), device="cuda")
+    table = _kv.dev(np.arange(6, dtype=np.int32).reshape(3, 2))
+    for start, before, want in (([0, 2, 2, 2], [0, 0, 0], "BAD_N"), ([0, 0, 0, 0], [0, -1, 0], "BAD_N"),
+                                ([3, 3, 3, 1], [0, 0, 0], "BAD_N"), ([5, 5, 5, 5], [0, 128, 7], None)):
+        pools = [_kv.dev(x) for x in _kv.make_pools(np.random.default_rng(0), 6, kvh, d)]
+        old = [x.clone() for x in pools]
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        spin.kv_append(cfg, new, new, _kv.dev(np.array(start, np.int32)), 0, _kv.dev(np.array(before, np.int32)), *pools,
+                       table, status)
+        assert int(status.item()) == (spin.STATUS_BITS[want] if want else 0)
+        assert all(torch.equal(x, y) for x, y in zip(pools, old))
+    # no new tokens at all: the arrays behind new_k and new_v are not looked at
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    spin.kv_append(cfg, new[:0], new[:0], _kv.dev(np.zeros(4, np.int32)), 0, _kv.dev(np.zeros(3, np.int32)), *pools, table,
+                   status)
+    assert int(status.item()) == 0 and all(torch.equal(x, y) for x, y in zip(pools, old))
