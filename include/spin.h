@@ -545,7 +545,8 @@ spin_status_t spin_kv_append(const spin_kv_config* cfg, const void* new_k, const
 /* Page management.  The state is the caller's: block_table int32 [n_req][bt_stride] (-1 = no
  * page) and ref int32 [n_pages], the number of table entries that use each page (0 = free).
  * Pools are any arrays indexed by page (this cache's, the indexer's keys and scales):
- * n_pools <= 16 host descriptors, data 4-byte aligned, page_bytes a multiple of 4.  Results
+ * n_pools <= 16 host descriptors, data 4-byte aligned, page_bytes a multiple of 4 up to 2^30; more
+ * arrays than that (a layer stack's) go to spin_pages_copy, 16 at a time.  Results
  * do not depend on the order in which threads run: fresh pages are the lowest free ones,
  * handed to requests in order.  A table entry outside [-1, n_pages) is treated as -1
  * (BAD_PAGE); releasing a page that has no reference leaves it at 0 (BAD_REF).
@@ -597,6 +598,14 @@ spin_status_t spin_pages_compact(int32_t n_req, int64_t n_pages, int32_t* block_
                                  int64_t bt_stride, int32_t* ref, const spin_page_pool* pools,
                                  int32_t n_pools, int32_t* n_live, void* workspace,
                                  size_t workspace_bytes, uint32_t* status, spin_stream_t stream);
+
+/* Repeats, in further pools, the page copies of the last spin_pages_reserve or spin_pages_compact that
+ * was given this workspace with the same n_req and n_pages: for caches of more than 16 arrays.  On
+ * the same stream, before any of these pages is written or the workspace is used again.  A workspace
+ * without such a call is invalid input; copies outside [0, n_pages) are left out (BAD_PAGE). */
+spin_status_t spin_pages_copy(int32_t n_req, int64_t n_pages, const spin_page_pool* pools, int32_t n_pools,
+                              void* workspace, size_t workspace_bytes, uint32_t* status,
+                              spin_stream_t stream);
 
 /* Version string of the library ("spin-gb300 <major>.<minor>.<patch> sm_103a"). */
 const char* spin_version(void);

@@ -691,6 +691,18 @@ spin_status_t spin_pages_reserve(int32_t n_req, int64_t n_pages, int32_t* block_
                     "spin_pages_reserve");
 }
 
+spin_status_t spin_pages_copy(int32_t n_req, int64_t n_pages, const spin_page_pool* pools, int32_t n_pools,
+                              void* workspace, size_t workspace_bytes, uint32_t* status, spin_stream_t stream) {
+    g_err[0] = 0;
+    if (n_req < 1 || n_req > 65535) return fail(SPIN_ERR_INVALID_ARG, "n_req %d outside [1, 65535]", n_req);
+    if (n_pages < 1 || n_pages > (1ll << 30)) return fail(SPIN_ERR_CAPACITY, "n_pages outside [1, 2^30]");
+    PagePoolSet set;
+    spin_status_t st = check_pools(pools, n_pools, n_req, n_pages, workspace, workspace_bytes, &set);
+    if (st) return st;
+    const PageTable t{n_req, n_pages, nullptr, 0, nullptr, status};
+    return launched(launch_pages_copy(t, set, workspace, (cudaStream_t)stream), "spin_pages_copy");
+}
+
 spin_status_t spin_pages_compact(int32_t n_req, int64_t n_pages, int32_t* block_table, int64_t bt_stride,
                                  int32_t* ref, const spin_page_pool* pools, int32_t n_pools, int32_t* n_live,
                                  void* workspace, size_t workspace_bytes, uint32_t* status, spin_stream_t stream) {

@@ -157,6 +157,7 @@ cudaError_t launch_pages_fork(const PageTable& t, const int32_t* table_in, const
 cudaError_t launch_pages_free(const PageTable& t, const int32_t* keep, cudaStream_t s);
 cudaError_t launch_pages_reserve(const PageTable& t, const int32_t* n_slots, const int32_t* n_new,
                                  const PagePoolSet& pools, int32_t* granted, void* ws, cudaStream_t s);
+cudaError_t launch_pages_copy(const PageTable& t, const PagePoolSet& pools, void* ws, cudaStream_t s);
 cudaError_t launch_pages_compact(const PageTable& t, const PagePoolSet& pools, int32_t* n_live, void* ws,
                                  cudaStream_t s);
 

@@ -312,8 +312,9 @@ __global__ void __launch_bounds__(kPlanThreads) pages_compact_kernel(PageTable t
 }
 
 // ------------------------------------------------------------------------------- copying
-// Pages src[k] -> dst[k] of every pool, in chunks of kCopyBytes.  No source is a destination.  After
-// a compaction's plan (REMAP) the table entries and reference counts follow first.
+// Pages src[k] -> dst[k] of every pool, in chunks of kCopyBytes.  No source is a destination, so that the
+// copies can be repeated for other pools (spin_pages_copy).  After a compaction's plan (REMAP) the table
+// entries and reference counts follow first.
 template <bool REMAP>
 __global__ void __launch_bounds__(kPgThreads) pages_copy_kernel(PageTable t, PagePoolSet pools, PagesWs w, int chunks) {
     pdl_begin();
@@ -332,12 +333,16 @@ __global__ void __launch_bounds__(kPgThreads) pages_copy_kernel(PageTable t, Pag
             t.ref[w.src[k]] = 0;
         }
     }
-    const int64_t items = (int64_t)*w.count * chunks;
+    const int64_t items = min((int64_t)max(*w.count, 0), t.n_pages) * chunks;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const int k = (int)(it / chunks);
         int c = (int)(it % chunks);
         const int32_t src = w.src[k], dst = w.dst[k];
-        if (src < 0) continue;
+        if (src == -1) continue;
+        if (src < 0 || src >= t.n_pages || dst < 0 || dst >= t.n_pages) {  // (no plan in this workspace)
+            set_status(t.status, SPIN_STATUS_BAD_PAGE);
+            continue;
+        }
         int p = 0;
         for (;; ++p) {
             const int n = (int)((pools.pool[p].page_bytes + kCopyBytes - 1) / kCopyBytes);
@@ -400,6 +405,10 @@ cudaError_t launch_pages_reserve(const PageTable& t, const int32_t* n_slots, con
     cudaError_t e = launch_pdl(pages_reserve_kernel, dim3(1), dim3(kPlanThreads), 0, s, nullptr, 0, t, n_slots, n_new,
                                granted, w);
     return e != cudaSuccess ? e : launch_copy<false>(t, pools, w, s);
+}
+
+cudaError_t launch_pages_copy(const PageTable& t, const PagePoolSet& pools, void* ws, cudaStream_t s) {
+    return launch_copy<false>(t, pools, pages_ws(ws, t.n_req, t.n_pages), s);
 }
 
 cudaError_t launch_pages_compact(const PageTable& t, const PagePoolSet& pools, int32_t* n_live, void* ws,

@@ -146,6 +146,7 @@ def lib():
             "spin_pages_fork": [i32, i64, P, i64, P, P, P, P, P],
             "spin_pages_free": [i32, i64, P, i64, P, P, P, P],
             "spin_pages_reserve": [i32, i64, P, i64, P, P, P, P, i32, P, P, ctypes.c_size_t, P, P],
+            "spin_pages_copy": [i32, i64, P, i32, P, ctypes.c_size_t, P, P],
             "spin_pages_compact": [i32, i64, P, i64, P, P, i32, P, P, ctypes.c_size_t, P, P],
             "spin_selftest_wait": [i32, u64, P, P, P],
             "spin_miss_curve": [P, i32, i64, P, P, i32, i32, P],
@@ -516,9 +517,13 @@ class CoreAttention:
                   self.workspace, status, stream)
 
 
+POOLS_A_CALL = 16          # page arrays that one C call moves
+
+
 class PagePools:
     """The arrays indexed by page that move with it: contiguous tensors [n_pages, ...] on one
-    device.  Keeps them alive; a layer stack lists every layer's."""
+    device, a page's bytes in each a multiple of 4.  Keeps them alive; a layer stack lists every layer's
+    (`groups`: their descriptors, as many as a call takes at a time)."""
 
     def __init__(self, *tensors):
         if not tensors:
@@ -528,11 +533,17 @@ class PagePools:
         self.device = tensors[0].get_device()
         if self.n_pages < 1:
             raise SpinError(1, "pools without pages")
+        descriptors = []
         for i, t in enumerate(tensors):
             if t.shape[0] != self.n_pages or t.get_device() != self.device or not t.is_contiguous() or not t.is_cuda:
                 raise SpinError(1, "pool %d: contiguous CUDA tensors of as many pages on one device" % i)
-        self.array = (SpinPagePool * len(tensors))(
-            *[SpinPagePool(t.data_ptr(), t.numel() // self.n_pages * t.element_size()) for t in tensors])
+            page_bytes = t.numel() // self.n_pages * t.element_size()
+            # (all of them before the first call: a later group's refusal would tear the pages apart)
+            if not 4 <= page_bytes <= 1 << 30 or page_bytes % 4 or t.data_ptr() % 4:
+                raise SpinError(1, "pool %d: a page's bytes must be a multiple of 4 in [4, 2^30], 4-byte aligned" % i)
+            descriptors.append(SpinPagePool(t.data_ptr(), page_bytes))
+        cut = [descriptors[i:i + POOLS_A_CALL] for i in range(0, len(descriptors), POOLS_A_CALL)]
+        self.groups = [(SpinPagePool * len(c))(*c) for c in cut]
 
 
 def pages_workspace(n_req: int, n_pages: int, device="cuda"):
@@ -545,7 +556,13 @@ def pages_workspace(n_req: int, n_pages: int, device="cuda"):
 def _pools_of(pools, n_pages, dev):
     if pools.n_pages != n_pages or pools.device != dev:
         raise SpinError(1, "the pools must have ref's %d pages and be on the current device" % n_pages)
-    return pools.array, len(pools.array)
+    return pools.groups[0], len(pools.groups[0])
+
+
+def _copy_rest(pools, n_req, ws, ws_bytes, status, s):
+    """The copies of the call before, in the arrays that it did not take."""
+    for g in pools.groups[1:]:
+        _check(lib().spin_pages_copy(n_req, pools.n_pages, g, len(g), ws, ws_bytes, status, s))
 
 
 def pages_fork(table_in, parent, table_out, ref, status, stream=None):
@@ -573,11 +590,13 @@ def pages_reserve(block_table, n_slots, n_new, ref, pools, granted, workspace, s
     dev = torch._C._cuda_getDevice()
     (R, bt), (n_pages,) = block_table.shape, ref.shape
     ws, ws_bytes = _workspace_arg(workspace, dev)
+    st, s = _status_arg(status, dev), _stream(stream)
     _check(lib().spin_pages_reserve(
         R, n_pages, _arg("block_table", block_table, torch.int32, (R, bt), dev), bt,
         _arg("n_slots", n_slots, torch.int32, (R,), dev), _arg("n_new", n_new, torch.int32, (R,), dev),
         _arg("ref", ref, torch.int32, (n_pages,), dev), *_pools_of(pools, n_pages, dev),
-        _arg("granted", granted, torch.int32, (R,), dev), ws, ws_bytes, _status_arg(status, dev), _stream(stream)))
+        _arg("granted", granted, torch.int32, (R,), dev), ws, ws_bytes, st, s))
+    _copy_rest(pools, R, ws, ws_bytes, st, s)
 
 
 def pages_compact(block_table, ref, pools, n_live, workspace, status, stream=None):
@@ -585,10 +604,12 @@ def pages_compact(block_table, ref, pools, n_live, workspace, status, stream=Non
     dev = torch._C._cuda_getDevice()
     (R, bt), (n_pages,) = block_table.shape, ref.shape
     ws, ws_bytes = _workspace_arg(workspace, dev)
+    st, s = _status_arg(status, dev), _stream(stream)
     _check(lib().spin_pages_compact(
         R, n_pages, _arg("block_table", block_table, torch.int32, (R, bt), dev), bt,
         _arg("ref", ref, torch.int32, (n_pages,), dev), *_pools_of(pools, n_pages, dev),
-        _arg("n_live", n_live, torch.int32, (1,), dev), ws, ws_bytes, _status_arg(status, dev), _stream(stream)))
+        _arg("n_live", n_live, torch.int32, (1,), dev), ws, ws_bytes, st, s))
+    _copy_rest(pools, R, ws, ws_bytes, st, s)
 
 
 # ------------------------------------------------------------------------ convenience

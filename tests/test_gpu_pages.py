@@ -272,3 +272,72 @@ def test_graph_replay():
         assert np.array_equal(granted.cpu().numpy(), gr) and int(live.item()) == nl
         assert np.array_equal(pool.cpu().numpy(), data[0])
     assert int(st.item()) == 0
+
+
+@pytest.mark.parametrize("count", [16, 17, 33, 244])
+def test_layer_stacks_of_many_arrays(count):
+    """More arrays than one C call takes move together all the same: reserve, then compact, of a stack of
+    layers' arrays of several sizes."""
+    rng = np.random.default_rng(count)
+    R, n_pages = 9, 60
+    lens = rng.integers(0, 400, R)
+    table, ref = state(rng, lens, n_pages, 8)
+    parent = rng.integers(-1, R, R)
+    table, ref = o.fork(table, parent, ref)
+    n = np.where(parent >= 0, lens[parent], 0)
+    add = rng.integers(0, 3, R) * rng.integers(1, 60, R)
+    pools = [p for i in range(count) for p in make_pools(rng, n_pages, [SHAPES[i % 5]])]
+    want, first = o.reserve(table, n, add, ref, pools_w := [p.copy() for p in pools]), sum(p.size for p in pools)
+    dt, dref, st = _kv.dev(table), _kv.dev(ref), status()
+    dp = [_kv.dev(p) for p in pools]
+    granted, live = torch.zeros(R, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    stack, ws = spin.PagePools(*dp), spin.pages_workspace(R, n_pages)
+    assert sum(p.page_bytes for g in stack.groups for p in g) * n_pages == first
+    spin.pages_reserve(dt, _kv.dev(n.astype(np.int32)), _kv.dev(add.astype(np.int32)), dref, stack, granted, ws, st)
+    assert np.array_equal(dt.cpu().numpy(), want[0]) and np.array_equal(dref.cpu().numpy(), want[1])
+    assert (want[0] != table).any()
+    for x, y in zip(dp, pools_w):
+        assert np.array_equal(x.cpu().numpy(), y)
+    # some leave, and the pool is made dense
+    t, rf = o.free(want[0], np.where(rng.random(R) < 0.5, 0, -1), want[1])
+    dt, dref = _kv.dev(t), _kv.dev(rf)
+    spin.pages_compact(dt, dref, stack, live, ws, st)
+    t, rf, n_live = o.compact(t, rf, pools_w)
+    assert np.array_equal(dt.cpu().numpy(), t) and np.array_equal(dref.cpu().numpy(), rf) and int(live.item()) == n_live
+    for x, y in zip(dp, pools_w):
+        assert np.array_equal(x.cpu().numpy(), y)
+    assert bool(st.item()) == (not want[2].all())
+
+
+def test_copies_outside_the_pool_are_left_out():
+    """A workspace that holds no plan: every copy it seems to ask for is checked."""
+    n_pages = 8
+    pool = torch.arange(n_pages, dtype=torch.int32, device="cuda")[:, None].repeat(1, 4)
+    old, group = pool.clone(), spin.PagePools(pool).groups[0]
+    ws = spin.pages_workspace(2, n_pages).view(torch.int32)
+    bad, ok = [-2, 8, -2 ** 31, 2 ** 31 - 1], [1, 1, 1, 1]
+    for dst, src, want in ((bad, ok, old), (ok, bad, old), (bad, bad, old), ([5, 6], [1, 2], None)):
+        for count in (len(dst), -1, 2 ** 31 - 1):
+            pool.copy_(old)
+            ws.fill_(-1)
+            ws[0] = count
+            ws[128:128 + len(dst)] = torch.tensor(dst, device="cuda")     # behind the header and the prefix
+            ws[192:192 + len(src)] = torch.tensor(src, device="cuda")
+            st = status()
+            rc = spin.lib().spin_pages_copy(2, n_pages, group, 1, ws.data_ptr(), ws.numel() * 4, st.data_ptr(), None)
+            torch.cuda.synchronize()
+            assert rc == 0
+            moved = old.clone()
+            if want is None and count > 0:
+                moved[5], moved[6] = old[1], old[2]
+            assert torch.equal(pool, moved)
+            assert int(st.item()) == (B["BAD_PAGE"] if want is not None and count > 0 else 0)
+
+
+def test_pools_whose_pages_cannot_be_copied_are_refused_together():
+    """Before the first call, wherever in the list they stand."""
+    good = [torch.zeros((4, 8), dtype=torch.uint8, device="cuda") for _ in range(20)]
+    for bad in (torch.zeros((4, 6), dtype=torch.uint8, device="cuda"), torch.zeros((4, 0), device="cuda"),
+                torch.zeros(33, dtype=torch.uint8, device="cuda")[1:].view(4, 8)):
+        with pytest.raises(spin.SpinError, match="pool 20"):
+            spin.PagePools(*good, bad)

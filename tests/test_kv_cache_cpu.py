@@ -230,3 +230,17 @@ def test_oracle_appends_infinities_beside_nothing_finite():
     assert pool[0, 0, 0].tolist() == [126, 254, 127] + [0] * 13 and scale[0, 0] == 0
     o.append(np.ones((1, 1, 16)), [0, 1], [1], pool, scale, np.zeros((1, 1), np.int32))
     assert (pool[0, 0, 0] & 127).tolist() == [0, 0, 127] + [0] * 13 and scale[0, 0] == 2.0 ** -8
+
+
+def test_page_copy_refusals(spin_lib):
+    L, pool, ws = spin.lib(), (spin.SpinPagePool * 1)(spin.SpinPagePool(256, 16)), 1 << 40
+
+    def copy(n_req=1, n_pages=4, pools=pool, n=1, w=A, b=ws):
+        return L.spin_pages_copy(n_req, n_pages, pools, n, w, b, None, None)
+
+    for kw, code in (({"n_req": 0}, 1), ({"n_req": 65536}, 1), ({"n_pages": 0}, 3), ({"n_pages": (1 << 30) + 1}, 3),
+                     ({"pools": None}, 1), ({"n": -1}, 1), ({"n": 17}, 1), ({"w": None}, 1), ({"b": 8}, 1),
+                     ({"w": ctypes.c_void_p(260)}, 1)):
+        assert copy(**kw) == code and err()
+    for data, nbytes in ((None, 16), (258, 16), (256, 0), (256, 6), (256, (1 << 30) + 4)):
+        assert copy(pools=(spin.SpinPagePool * 1)(spin.SpinPagePool(data, nbytes))) == 1 and "pool 0" in err()
