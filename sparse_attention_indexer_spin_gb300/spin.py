@@ -505,6 +505,24 @@ class CoreAttention:
         self.row_slots = torch.zeros(shape[:2], dtype=torch.int32, device=device)
         self.workspace = kv_workspace(cfg, rows, top_k, device)
 
+    def check(self, q, block_table, n_slots, topk_idx, status):
+        """Refuses arguments that attend() would refuse, without a launch."""
+        cfg, dev = self.cfg, torch._C._cuda_getDevice()
+        R, shape = cfg.n_req, (cfg.n_req, self.rows, cfg.n_heads, cfg.head_dim)
+        if _arg("core_q", q, TORCH_DTYPE[cfg.dtype], shape, dev) % 16:
+            raise SpinError(1, "core_q must be 16-byte aligned")
+        _kv_pool_args(cfg, *self.cache.tensors, block_table, dev)
+        if 64 * block_table.shape[-1] < cfg.max_slots:
+            raise SpinError(2, "block_table holds %d slots a request, the core attention's max_slots is %d" % (
+                64 * block_table.shape[-1], cfg.max_slots))
+        _arg("n_slots", n_slots, torch.int32, (R,), dev)
+        if topk_idx is not None:
+            _arg("topk_idx", topk_idx, torch.int32, (R, self.rows, topk_idx.shape[-1]), dev)
+            if not 1 <= topk_idx.shape[-1] <= 16384:
+                raise SpinError(1, "the core attention takes 1 to 16384 listed slots, got %d" % topk_idx.shape[-1])
+        _arg("out", self.out, q.dtype, shape, dev)
+        _status_arg(status, dev)
+
     def attend(self, q, block_table, n_slots, topk_idx, status, stream=None):
         """Every row of request r sees its n_slots[r] slots (the indexer's verifier rows do), or the
         listed ones of them."""
@@ -660,6 +678,10 @@ def run_step(cfg, state: LayerState, buf: StepBuffers, q, w, k_pool, k_scale, n_
     replaces the plain one.  With a CoreAttention (of top_k = cfg.top_k) its queries core_q then
     attend to the top-K slots of its cache, whose pages block_table names too: core.out, core.lse."""
     rows = buf.rows
+    if core is not None:  # before anything is launched: a step is not to stop halfway
+        if core_q is None:
+            raise SpinError(1, "core needs its queries core_q")
+        core.check(core_q, block_table, n_slots, buf.topk, buf.status)
     union = buf.union if rows > 1 else None
     n_union = buf.n_union if rows > 1 else None
     if block_age is None:

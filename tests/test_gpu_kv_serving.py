@@ -182,3 +182,34 @@ def test_two_streams_at_once():
         spin.kv_append(*args, *tail, stream=streams[2])
     torch.cuda.synchronize()
     assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1]) and torch.equal(other.k, codes)
+
+
+def test_a_step_with_a_wrong_core_attention_launches_nothing():
+    wl = syn.CONFIGS["pr1"].replace(steps=2, n_layers=1, n_req=3, n0=500, top_k=64)
+    inp, cfg = syn.SyntheticInputs(wl, "cuda"), spin.make_config(**wl.config_fields())
+    st, buf = spin.LayerState(cfg), spin.StepBuffers(cfg, 1)
+    spin.init_state(cfg, st.V, st.D, st.Vmax, st.warm)
+    q, w, qp = inp.step_inputs()
+    torch.cuda.synchronize()
+    want = [x.clone() for x in (st.V, st.D, st.Vmax, st.warm, buf.blocks, buf.n_blocks, buf.topk, buf.scores)]
+
+    def core(max_slots=wl.max_slots, rows=1, pages=inp.n_pages):
+        return spin.CoreAttention(spin.make_kv_config(3, max_slots, rows, 16, 2, 64, "bf16"), spin.KvCache(pages, 2, 64),
+                                  rows, wl.top_k)
+
+    def step(c, cq, table=inp.block_table):
+        spin.run_step(cfg, st, buf, q, w, inp.k_pool[0], inp.k_scale[0], inp.n_pages, table, inp.n_slots, qp, 0, 0,
+                      core=c, core_q=cq)
+
+    good = torch.zeros((3, 1, 16, 64), dtype=torch.bfloat16, device="cuda")
+    odd = torch.zeros(good.numel() + 1, dtype=torch.bfloat16, device="cuda")[1:].view(good.shape)
+    for c, cq in ((core(), None), (core(), good.float()), (core(), good[:2]), (core(), good.cpu()), (core(), odd),
+                  (core(rows=2), good.repeat(1, 2, 1, 1)), (core(max_slots=1 << 24), good)):
+        with pytest.raises(spin.SpinError):
+            step(c, cq)
+    torch.cuda.synchronize()
+    for x, y in zip((st.V, st.D, st.Vmax, st.warm, buf.blocks, buf.n_blocks, buf.topk, buf.scores), want):
+        assert torch.equal(x, y)
+    step(core(), good)
+    torch.cuda.synchronize()
+    assert int(buf.status.item()) == 0 and not torch.equal(buf.topk, want[6])

@@ -244,3 +244,13 @@ def test_page_copy_refusals(spin_lib):
         assert copy(**kw) == code and err()
     for data, nbytes in ((None, 16), (258, 16), (256, 0), (256, 6), (256, (1 << 30) + 4)):
         assert copy(pools=(spin.SpinPagePool * 1)(spin.SpinPagePool(data, nbytes))) == 1 and "pool 0" in err()
+
+
+def test_run_step_refuses_a_core_attention_without_queries(monkeypatch):
+    """As an error of the binding, before anything is launched."""
+    for name in ("select_blocks", "indexer_score", "topk", "update_ema"):
+        monkeypatch.setattr(spin, name, lambda *a, **k: pytest.fail("launched"))
+    core, buf = object.__new__(spin.CoreAttention), object.__new__(spin.StepBuffers)
+    buf.rows = 1
+    with pytest.raises(spin.SpinError, match="core_q"):
+        spin.run_step(None, None, buf, None, None, None, None, 0, None, None, None, core=core)
