@@ -472,6 +472,7 @@ spin_status_t spin_workspace_size(const spin_config* cfg, int32_t rows, size_t* 
  *                   g * n_heads/kv_heads ... share key/value head g
  *   lse             float [R][rows][n_heads], natural log; may be NULL
  *   topk_idx        int32 [R][rows][top_k] slot ids in any order, -1 = none; NULL: every slot
+ * Arrays of int32 and float, and status, are 4-byte aligned (here and in the page calls).
  * ------------------------------------------------------------------------------------------ */
 typedef struct spin_kv_config {
     int32_t n_req;        /* 1 .. 65535 */

@@ -7,6 +7,7 @@
 #include <stdio.h>
 
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 
 #include <cmath>
@@ -546,6 +547,13 @@ static spin_status_t check_kv_rows(const spin_kv_config* c, int32_t rows, int32_
     return SPIN_OK;
 }
 
+// Words that a kernel reads or writes one at a time (NULL passes): an odd address would fault there.
+static bool words_aligned(std::initializer_list<const void*> words) {
+    uintptr_t bits = 0;
+    for (const void* p : words) bits |= (uintptr_t)p;
+    return (bits & 3) == 0;
+}
+
 static spin_status_t check_kv_pools(const spin_kv_config* c, const void* k_pool, const void* v_pool,
                                     const float* k_scale, const float* v_scale, int64_t n_pages,
                                     const int32_t* block_table, int64_t bt_stride) {
@@ -585,6 +593,8 @@ spin_status_t spin_kv_attend(const spin_kv_config* cfg, const void* q, const uin
         return fail(SPIN_ERR_INVALID_ARG, "topk_idx and top_k > 0 go together");
     if ((((uintptr_t)q | (uintptr_t)out) & 15) != 0)
         return fail(SPIN_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
+    if (!words_aligned({n_slots, topk_idx, lse, status}))
+        return fail(SPIN_ERR_INVALID_ARG, "n_slots, topk_idx, lse and status must be 4-byte aligned");
     const size_t need = kv_attend_workspace_bytes(*cfg, rows, top_k);
     if (!workspace || workspace_bytes < need)
         return fail(SPIN_ERR_INVALID_ARG, "workspace of %zu bytes needed (got %zu)", need, workspace_bytes);
@@ -608,6 +618,8 @@ spin_status_t spin_kv_append(const spin_kv_config* cfg, const void* new_k, const
         return fail(SPIN_ERR_INVALID_ARG, "max_new %d outside [0, max_slots=%d]", max_new, cfg->max_slots);
     if ((((uintptr_t)new_k | (uintptr_t)new_v) & 15) != 0)
         return fail(SPIN_ERR_INVALID_ARG, "new_k and new_v must be 16-byte aligned");
+    if (!words_aligned({new_start, n_before, status}))
+        return fail(SPIN_ERR_INVALID_ARG, "new_start, n_before and status must be 4-byte aligned");
     KvAppendArgs a{{new_k, new_v}, {k_pool, v_pool}, {k_scale, v_scale}, n_tokens, new_start, max_new, n_before,
                    n_pages, block_table, bt_stride, status};
     return launched(launch_kv_append(*cfg, a, (cudaStream_t)stream), "spin_kv_append");
@@ -661,6 +673,8 @@ spin_status_t spin_pages_fork(int32_t n_req, int64_t n_pages, const int32_t* tab
     spin_status_t st = check_pages(n_req, n_pages, table_out, bt_stride, ref);
     if (st) return st;
     if (!table_in || !parent) return fail(SPIN_ERR_INVALID_ARG, "table_in and parent must be non-NULL");
+    if (!words_aligned({table_in, parent, status}))
+        return fail(SPIN_ERR_INVALID_ARG, "table_in, parent and status must be 4-byte aligned");
     const uintptr_t in = (uintptr_t)table_in, out = (uintptr_t)table_out, bytes = (uintptr_t)n_req * bt_stride * 4;
     if (in != out && in < out + bytes && out < in + bytes)
         return fail(SPIN_ERR_INVALID_ARG, "table_in and table_out overlap");
@@ -673,6 +687,8 @@ spin_status_t spin_pages_free(int32_t n_req, int64_t n_pages, int32_t* block_tab
     spin_status_t st = check_pages(n_req, n_pages, block_table, bt_stride, ref);
     if (st) return st;
     if (!keep_slots) return fail(SPIN_ERR_INVALID_ARG, "keep_slots is NULL");
+    if (!words_aligned({keep_slots, status}))
+        return fail(SPIN_ERR_INVALID_ARG, "keep_slots and status must be 4-byte aligned");
     const PageTable t{n_req, n_pages, block_table, bt_stride, ref, status};
     return launched(launch_pages_free(t, keep_slots, (cudaStream_t)stream), "spin_pages_free");
 }
@@ -684,6 +700,8 @@ spin_status_t spin_pages_reserve(int32_t n_req, int64_t n_pages, int32_t* block_
     spin_status_t st = check_pages(n_req, n_pages, block_table, bt_stride, ref);
     if (st) return st;
     if (!n_slots || !n_new || !granted) return fail(SPIN_ERR_INVALID_ARG, "n_slots, n_new and granted must be non-NULL");
+    if (!words_aligned({n_slots, n_new, granted, status}))
+        return fail(SPIN_ERR_INVALID_ARG, "n_slots, n_new, granted and status must be 4-byte aligned");
     PagePoolSet set;
     if ((st = check_pools(pools, n_pools, n_req, n_pages, workspace, workspace_bytes, &set))) return st;
     const PageTable t{n_req, n_pages, block_table, bt_stride, ref, status};
@@ -699,6 +717,7 @@ spin_status_t spin_pages_copy(int32_t n_req, int64_t n_pages, const spin_page_po
     PagePoolSet set;
     spin_status_t st = check_pools(pools, n_pools, n_req, n_pages, workspace, workspace_bytes, &set);
     if (st) return st;
+    if (!words_aligned({status})) return fail(SPIN_ERR_INVALID_ARG, "status must be 4-byte aligned");
     const PageTable t{n_req, n_pages, nullptr, 0, nullptr, status};
     return launched(launch_pages_copy(t, set, workspace, (cudaStream_t)stream), "spin_pages_copy");
 }
@@ -709,6 +728,8 @@ spin_status_t spin_pages_compact(int32_t n_req, int64_t n_pages, int32_t* block_
     spin_status_t st = check_pages(n_req, n_pages, block_table, bt_stride, ref);
     if (st) return st;
     if (!n_live) return fail(SPIN_ERR_INVALID_ARG, "n_live is NULL");
+    if (!words_aligned({n_live, status}))
+        return fail(SPIN_ERR_INVALID_ARG, "n_live and status must be 4-byte aligned");
     PagePoolSet set;
     if ((st = check_pools(pools, n_pools, n_req, n_pages, workspace, workspace_bytes, &set))) return st;
     const PageTable t{n_req, n_pages, block_table, bt_stride, ref, status};

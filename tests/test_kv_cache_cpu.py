@@ -254,3 +254,37 @@ def test_run_step_refuses_a_core_attention_without_queries(monkeypatch):
     buf.rows = 1
     with pytest.raises(spin.SpinError, match="core_q"):
         spin.run_step(None, None, buf, None, None, None, None, 0, None, None, None, core=core)
+
+
+def test_words_at_odd_addresses_are_refused(spin_lib):
+    """Every array of 4-byte words, one at a time (an odd address would fault on the device)."""
+    L, cfg, odd, ws = spin.lib(), cfg_of(), ctypes.c_void_p(258), 1 << 40
+    pool = (spin.SpinPagePool * 1)(spin.SpinPagePool(256, 16))
+    far = ctypes.c_void_p(1 << 30)
+
+    def attend(n=A, idx=A, lse=A, status=A):
+        return L.spin_kv_attend(cfg, A, A, A, A, A, 4, A, 2, n, 1, idx, 1, A, lse, A, ws, status, None)
+
+    def append(start=A, before=A, status=A):
+        return L.spin_kv_append(cfg, A, A, 1, start, 1, before, A, A, A, A, 4, A, 2, status, None)
+
+    def fork(table_in=far, parent=A, status=A):
+        return L.spin_pages_fork(1, 4, table_in, 2, parent, A, A, status, None)
+
+    def free(keep=A, status=A):
+        return L.spin_pages_free(1, 4, A, 2, keep, A, status, None)
+
+    def reserve(n=A, new=A, granted=A, status=A):
+        return L.spin_pages_reserve(1, 4, A, 2, n, new, A, pool, 1, granted, A, ws, status, None)
+
+    def compact(live=A, status=A):
+        return L.spin_pages_compact(1, 4, A, 2, A, pool, 1, live, A, ws, status, None)
+
+    def copy(status=A):
+        return L.spin_pages_copy(1, 4, pool, 1, A, ws, status, None)
+
+    for f in (attend, append, fork, free, reserve, compact, copy):
+        names = f.__code__.co_varnames[:f.__code__.co_argcount]
+        for name in names:
+            at = ctypes.c_void_p((1 << 30) + 2) if name == "table_in" else odd
+            assert f(**{name: at}) == 1 and "4-byte aligned" in err(), (f.__name__, name)
