@@ -449,3 +449,44 @@ def test_a_nan_value_does_not_slow_the_call_down():
     got = out.isnan().cpu().numpy()
     assert got.sum() == 2 * heads // kvh and got[0, 1, :heads // kvh, 5].all() and got[0, 3, :heads // kvh, 5].all()
     assert times[1] <= 2 * times[0] + 0.05, times
+
+
+def test_long_rows_keep_the_second_term_of_fp32_weights():
+    """40000 slots of which four take most of the weight, against bounds that do not grow with n.  Scores
+    come from one dimension, so that their dot products are exact: |ds| <= es = 4 x 2^-22 S + 2^-22
+    (|s| + 8).  The row is divided over the GPU (a CTA an SM at least takes part, or four units of 64 slots
+    each): a warp adds up ceil(units / 2) tiles with at most 12 roundings each, and a join every fourth of
+    at most 158 pieces, so that sums are off by el = (12 tiles + 40 + 16) 2^-22.  The same weights
+    rounded to one f16 term lie outside these bounds."""
+    rng = np.random.default_rng(5)
+    n, heads, d = 40000, 16, 64
+    n_pages = -(-n // 64)
+    k = np.zeros((n_pages, 64, 1, d), np.uint8)
+    k[..., 3] = o.e4m3_encode(rng.uniform(0, 8, (n_pages, 64, 1)))
+    for i, c in zip(rng.choice(n, 4, replace=False), (24.0, 26.0, 28.0, 28.0)):
+        k[i // 64, i % 64, 0, 3] = o.e4m3_encode([c])[0]
+    v = o.e4m3_encode(np.clip(rng.normal(size=(n_pages, 64, 1, d)) * 100, -448, 448))
+    pools = [k, v, np.ones((n_pages, 1), np.float32), np.full((n_pages, 1), 0.01, np.float32)]
+    q = np.zeros((1, 1, heads, d))
+    q[..., 3] = rng.uniform(0.5, 0.7, heads).astype(np.float32)
+    table, ns = rng.permutation(n_pages)[None].astype(np.int32), np.array([[n]], np.int32)
+    cfg = spin.make_kv_config(1, n, 1, heads, 1, d, "f32", 1.0)
+    out, lse = _kv.run_attend(cfg, torch.from_numpy(q).float().cuda(), [_kv.dev(x) for x in pools], _kv.dev(table),
+                              _kv.dev(ns), 1)
+    ref, rlse, info = o.attend(q, *pools, table, ns, 1.0)
+    cost = n_pages + 4
+    ranks = min(torch.cuda.get_device_properties(0).multi_processor_count, -(-cost // 4))
+    tiles = -(-(-(-cost // ranks)) // 2)
+    es = (4 * info["S"] + info["smax"] + 8) * 2.0 ** -22
+    el = (12 * tiles + 40 + 16) * 2.0 ** -22
+    tol = (2 * es + 2.0 ** -21 + 2 * el)[..., None] * info["A"] + 2.0 ** -24 * np.abs(ref)
+    tol += (n * 2.0 ** -37 * info["top"] * 448)[..., None]
+    assert (np.abs(out.double().cpu().numpy() - ref) <= tol).all()
+    assert (np.abs(lse.double().cpu().numpy() - rlse) <= es + el + 2.0 ** -22 * (np.abs(rlse) + 1)).all()
+    # one term of 11 bits instead of two
+    i = np.arange(n)
+    kc, vv = o.E4M3[k[table[0, i // 64], i % 64, 0]], o.E4M3[v[table[0, i // 64], i % 64, 0]] * float(pools[3][0, 0])
+    t = kc @ q[0, 0].T * np.log2(np.e)
+    w = np.exp2(t - t.max(0) + 12)
+    one = (w.astype(np.float16).astype(float).T @ vv) / w.sum(0)[:, None]
+    assert (np.abs(one - ref[0, 0]) > tol[0, 0]).any()
