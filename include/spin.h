@@ -530,7 +530,8 @@ spin_status_t spin_kv_attend(const spin_kv_config* cfg, const void* q, const uin
  * beside nothing finite but zeros thus count as 0, the scale being 0).
  * Scales only grow within a page, and a page's content does not depend on what was in it before
  * its slot 0 was written.  With power-of-two scales both are exact up to the e4m3 rounding.  Slots
- * behind the new ones are left as they are.  Requests must not share a page they append to (spin_pages_reserve).
+ * behind the new ones are left as they are.  Requests must not share a page they append to
+ * (spin_pages_reserve), nor one request hold a page twice in the blocks that its new slots fall in.
  * max_new: the largest count of new tokens of a request (sizes the launch).
  * Checked on the device: new_start not ascending within [0, n_tokens], a count above max_new,
  * n_before < 0 or past max_slots with the new ones (BAD_N, the request is skipped; where

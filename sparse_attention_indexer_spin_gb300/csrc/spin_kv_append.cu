@@ -9,11 +9,12 @@
 // most half a step, 2^-4 of a normal code), and moving the earlier slots to a larger scale
 // loses only what falls below e4m3's smallest subnormal.
 //
-// Memory bounds it: each new value is read once and its code written once.  45056 bf16 tokens of 8
-// heads x 128 (8 prompts): 53 us, 5.2 TB/s of the 277 MB; f32 92 us; 8 x 64 33 us.  Issue slots come
-// next, so maxima are taken two values at a time, a thread divides once for its place, and keys and
-// values share a CTA's look-up (81 us before).  A token each for 64 requests: 11 us in a graph, the
-// chain of dependent reads counts -> page -> scale.
+// Memory bounds it: each new value is read once and its code written once.  Eight ragged prompts of bf16
+// tokens, 8 heads x 128, one call among others: 49 us, 6.0 TB/s of the 293 MB.  As a graph launch of its own
+// behind an L2 flush, some microseconds of it the launch: 45056 tokens of that shape 53 us (277 MB), f32 92 us,
+// 8 x 64 33 us.  Issue slots come next, so maxima are taken two values at a time, a thread divides once for
+// its place, and keys and values share a CTA's look-up (81 us before).  A token each for 64 requests: 11 us
+// in such a graph, the chain of dependent reads counts -> page -> scale.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 

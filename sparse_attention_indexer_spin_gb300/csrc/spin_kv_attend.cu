@@ -25,17 +25,18 @@
 // The codes have to become f16 in registers anyway, on their way from shared memory to the
 // products, and 16 or 32 query rows fill an m16 tile but an eighth or a quarter of a tcgen05 one:
 // such a kernel (codes converted into shared memory, o in tensor memory) was built and took 511 us
-// where this takes 396, its hand-offs between converting, multiplying and weighting warps alone
-// 3100 cycles a tile of 128 slots.
+// where this takes 398, its hand-offs between converting, multiplying and weighting warps alone
+// 3100 cycles a tile of 128 slots.  Products of unconverted codes, with queries and weights as sums of e4m3
+// terms, have not been tried.
 //
 // What bounds it (one GB300, D = 128): memory where few query rows share a key head, and then the
 // ends of the launch (its start 2 us, CTAs that end up to a tenth apart, the join 6.5 us); above
 // some 16 rows a key head the products: a scheduler has two warps to choose from, the tensor pipe
 // is active 45 % of the time and conversions take a third of the issue slots.
-//   1 request of 131072 slots, 64 heads on 8:          56 us, 4.8 TB/s (6.7 TB/s a slot more)
-//   64 requests of 100 to 8192 slots, 32 heads on 8:   54 us, 4.5 TB/s
-//   16 of 4096 to 32768, 4 rows of 64 heads on 8, f16: 119 us, 3.9 TB/s
-//   32 of 100000 to 131072, 64 heads on one:           396 us, 2.4 TB/s, 0.3 PFLOP/s
+//   1 request of 131072 slots, 64 heads on 8:          55 us, 4.9 TB/s (6.7 TB/s a slot more)
+//   64 requests of 100 to 8192 slots, 32 heads on 8:   55 us, 4.5 TB/s
+//   16 of 4096 to 32768, 4 rows of 64 heads on 8, f16: 120 us, 3.9 TB/s
+//   32 of 100000 to 131072, 64 heads on one:           399 us, 2.4 TB/s, 0.3 PFLOP/s
 //   96 requests, 512 listed slots, 64 heads on one:    22 us, list -> page -> code in turn;
 //     2048 listed slots: 53 us, a tile's chain of dependent instructions
 #include "spin_kv_attend.cuh"
@@ -52,7 +53,11 @@ constexpr int kAtUnit = 64;      // slots in a unit of work
 constexpr int kAtJobUnits = 4;
 // A job is split unless whole jobs cost at most this many units more on the busiest CTA: the
 // joining launch costs about as much (6.5 us; a unit takes 1.1 us with the GPU full,
-// less where it is not).
+// less where it is not).  No value is best everywhere: with 5, lists of 64-wide heads took 46.7 us
+// instead of 40, and 40 requests of mixed lengths 33.9 instead of 37.8.  The host knows max_slots and not
+// the lengths, so that short contexts under a large max_slots are divided for nothing: 64 requests
+// of 100 to 700 slots, 64 heads on one, 23 us under 700 and 29 under 131072 (a launch of its own, cold
+// cache).
 constexpr int kAtSplitGain = 12;
 
 // ------------------------------------------------------------------------ small helpers
