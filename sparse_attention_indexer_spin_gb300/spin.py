@@ -571,6 +571,13 @@ def pages_workspace(n_req: int, n_pages: int, device="cuda"):
     return torch.empty(int(out.value), dtype=torch.uint8, device=device)
 
 
+def _table_shape(table, ref):
+    if table.dim() != 2 or ref.dim() != 1:
+        raise SpinError(2, "a block table has shape [n_req][blocks] and ref [n_pages]; got %s and %s" % (
+            tuple(table.shape), tuple(ref.shape)))
+    return (*table.shape, ref.shape[0])
+
+
 def _pools_of(pools, n_pages, dev):
     if pools.n_pages != n_pages or pools.device != dev:
         raise SpinError(1, "the pools must have ref's %d pages and be on the current device" % n_pages)
@@ -585,8 +592,8 @@ def _copy_rest(pools, n_req, ws, ws_bytes, status, s):
 
 def pages_fork(table_in, parent, table_out, ref, status, stream=None):
     """spin_pages_fork: row r of table_out becomes row parent[r] of table_in (-1: empty)."""
+    R, bt, n_pages = _table_shape(table_out, ref)
     dev = torch._C._cuda_getDevice()
-    (R, bt), (n_pages,) = table_out.shape, ref.shape
     _check(lib().spin_pages_fork(
         R, n_pages, _arg("table_in", table_in, torch.int32, (R, bt), dev), bt,
         _arg("parent", parent, torch.int32, (R,), dev), _arg("table_out", table_out, torch.int32, (R, bt), dev),
@@ -595,8 +602,8 @@ def pages_fork(table_in, parent, table_out, ref, status, stream=None):
 
 def pages_free(block_table, keep_slots, ref, status, stream=None):
     """spin_pages_free: request r keeps the pages of its first keep_slots[r] slots (< 0: all)."""
+    R, bt, n_pages = _table_shape(block_table, ref)
     dev = torch._C._cuda_getDevice()
-    (R, bt), (n_pages,) = block_table.shape, ref.shape
     _check(lib().spin_pages_free(
         R, n_pages, _arg("block_table", block_table, torch.int32, (R, bt), dev), bt,
         _arg("keep_slots", keep_slots, torch.int32, (R,), dev), _arg("ref", ref, torch.int32, (n_pages,), dev),
@@ -605,8 +612,8 @@ def pages_free(block_table, keep_slots, ref, status, stream=None):
 
 def pages_reserve(block_table, n_slots, n_new, ref, pools, granted, workspace, status, stream=None):
     """spin_pages_reserve: makes the next n_new[r] slots of every request writable."""
+    R, bt, n_pages = _table_shape(block_table, ref)
     dev = torch._C._cuda_getDevice()
-    (R, bt), (n_pages,) = block_table.shape, ref.shape
     ws, ws_bytes = _workspace_arg(workspace, dev)
     st, s = _status_arg(status, dev), _stream(stream)
     _check(lib().spin_pages_reserve(
@@ -619,8 +626,8 @@ def pages_reserve(block_table, n_slots, n_new, ref, pools, granted, workspace, s
 
 def pages_compact(block_table, ref, pools, n_live, workspace, status, stream=None):
     """spin_pages_compact: moves the used pages to the lowest ids; n_live int32 [1]."""
+    R, bt, n_pages = _table_shape(block_table, ref)
     dev = torch._C._cuda_getDevice()
-    (R, bt), (n_pages,) = block_table.shape, ref.shape
     ws, ws_bytes = _workspace_arg(workspace, dev)
     st, s = _status_arg(status, dev), _stream(stream)
     _check(lib().spin_pages_compact(

@@ -288,3 +288,13 @@ def test_words_at_odd_addresses_are_refused(spin_lib):
         for name in names:
             at = ctypes.c_void_p((1 << 30) + 2) if name == "table_in" else odd
             assert f(**{name: at}) == 1 and "4-byte aligned" in err(), (f.__name__, name)
+
+
+def test_page_calls_refuse_tables_and_counts_of_other_dimensions():
+    t, ref, x = torch.zeros((2, 3), dtype=torch.int32), torch.zeros(4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for table, r in ((t[0], ref), (t[None], ref), (t, ref[None])):
+        for call in (lambda: spin.pages_fork(table, x, table, r, None), lambda: spin.pages_free(table, x, r, None),
+                     lambda: spin.pages_reserve(table, x, x, r, None, x, x, None),
+                     lambda: spin.pages_compact(table, r, None, x, x, None)):
+            with pytest.raises(spin.SpinError, match="block table"):
+                call()
