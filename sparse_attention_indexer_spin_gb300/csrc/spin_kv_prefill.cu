@@ -463,6 +463,7 @@ prefill_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_constant
                     if (primed && !border && !far && !sc.odd) {
                         // Every row has a reference, and most pages do not exceed it: their weights are taken at once.  A
                         // sum that f16 holds says that none of them left its range; else the page is done again below.
+                        // (c may be infinite here: scores that are not below zero leave the range then.)
                         float s[kBlock];
                         tm_ld32(tS, s);
                         tm_ld32(tS + 32, s + 32);
@@ -504,6 +505,12 @@ prefill_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_constant
                     tm_ld32(tS + 32, s + 32);
                     tm_wait32(s);
                     tm_wait32(s + 32);
+                    if (fabsf(c) == __uint_as_float(0x7f800000u)) {
+                        // an overflow of the factors' product is no score's: keys of zero score 0 whatever their scale
+#pragma unroll
+                        for (int x = 0; x < kBlock; ++x) s[x] *= sc.ks;
+                        c = qs;
+                    }
                     if (border) {
 #pragma unroll
                         for (int x = 0; x < kBlock; ++x) s[x] = x < n ? s[x] * c : ninf;
