@@ -500,9 +500,9 @@ typedef struct spin_kv_config {
  * them) do not reach its outputs; a NaN code inside it does.  Products are exact, and sums, softmax weights' sums and the running
  * maximum are fp32; the weights enter their product with the values as one f16 term for
  * BF16 and F16, as two (22 bits) for F32, and queries as one f16 term scaled by a power of two per
- * row (BF16, F16) or two (F32).  Value scales are to be at most 2^100 in magnitude, and a row's
- * within a factor of 2^110 of each other (0 counts as 2^-100): beyond that a weight may overflow,
- * or small ones be lost from the sum.
+ * row (BF16, F16) or two (F32).  Scores are fp32: one beyond 2^127 counts as infinite.  Key scales are to be at most 2^95
+ * in magnitude, value scales at most 2^100, and a row's value scales within a factor of 2^110 of each other (0 counts as
+ * 2^-100): beyond that a weight may overflow, or small ones be lost from the sum.
  *
  * Checked on the device: n_slots outside [0, max_slots] (BAD_N, the row counts as empty), a
  * list entry outside [-1, n_slots) (BAD_LIST) and a slot whose page is outside [0, n_pages)

@@ -33,12 +33,15 @@
 // ends of the launch (its start 2 us, CTAs that end up to a tenth apart, the join 6.5 us); above
 // some 16 rows a key head the products: a scheduler has two warps to choose from, the tensor pipe
 // is active 45 % of the time and conversions take a third of the issue slots.
-//   1 request of 131072 slots, 64 heads on 8:          55 us, 4.9 TB/s (6.7 TB/s a slot more)
+//   1 request of 131072 slots, 64 heads on 8:          56 us, 4.8 TB/s (6.7 TB/s a slot more)
 //   64 requests of 100 to 8192 slots, 32 heads on 8:   55 us, 4.5 TB/s
 //   16 of 4096 to 32768, 4 rows of 64 heads on 8, f16: 120 us, 3.9 TB/s
-//   32 of 100000 to 131072, 64 heads on one:           399 us, 2.4 TB/s, 0.3 PFLOP/s
+//   32 of 100000 to 131072, 64 heads on one:           402 us, 2.4 TB/s, 0.3 PFLOP/s
 //   96 requests, 512 listed slots, 64 heads on one:    22 us, list -> page -> code in turn;
 //     2048 listed slots: 53 us, a tile's chain of dependent instructions
+#include <algorithm>
+#include <limits>
+
 #include "spin_kv_attend.cuh"
 
 namespace spin {
@@ -426,18 +429,23 @@ kv_attend_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_consta
                 for (int i = 0; i < MT; ++i)
 #pragma unroll
                     for (int r = 0; r < 2; ++r) c[i][r] = qs[i][r] * ks;
-                if (border) {
+                // an overflow of qs ks is no score's (keys of zero score 0 whatever their scale): a scale that could bring it
+                // about is taken first (s is below 2^32)
+                const bool large = !(fabsf(ks) < plan.most_ks);
+                if (border || large) {
+                    const float k1 = large ? ks : 1.0f;
 #pragma unroll
                     for (int i = 0; i < MT; ++i)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
+                            if (large) c[i][r] = qs[i][r];
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
 #pragma unroll
                                 for (int x = 2 * r; x < 2 * r + 2; ++x) {
                                     const int at_slot = 8 * j + 2 * t4 + (x & 1);
                                     const bool ok = ((mask >> at_slot) & 1u) && slot0 + at_slot < nlim[i][r];
-                                    s[i][j][x] = ok ? s[i][j][x] * c[i][r] : ninf;
+                                    s[i][j][x] = ok ? s[i][j][x] * k1 * c[i][r] : ninf;
                                 }
                             c[i][r] = 1.0f;
                         }
@@ -756,6 +764,8 @@ static cudaError_t launch_at(const spin_kv_config& cfg, const KvAttendArgs& a, c
     p.by_job = jobs <= G;
     p.owner = reinterpret_cast<int4*>(a.workspace);
     p.rec = a.workspace + ((size_t)kAtMostCtas * device_sm_count() * sizeof(int4) + 255) / 256 * 64;
+    // (a row's qs is 2^114 softmax_scale log2(e) at most)
+    p.most_ks = std::min(std::numeric_limits<float>::max(), 0x1p13f / fabsf(cfg.softmax_scale * 1.4426950408889634f));
     e = launch_pdl(k, dim3(G), dim3(kAtThreads), L::kBytes, s, nullptr, 0, cfg, a, p);
     if (e != cudaSuccess || !p.split) return e;
     return launch_pdl(kv_attend_join_kernel<T, D>, dim3(p.by_job ? (unsigned)jobs : G, M < L::kRows ? M : L::kRows),

@@ -106,6 +106,7 @@ struct AtPlan {
     float* rec;     // partial results, two records per CTA: crows x D sums, then (reference, l) of each row
     int4* owner;    // a divided job (request, job of the request), its first rank and number of pieces (by_job:
                     // of this job; else: of the job that this CTA begins and does not finish); w = 0: none
+    float most_ks;  // key scales below this leave a row's factor times them finite
 };
 
 constexpr int kAtMinCost = 4;      // cost a rank takes at least, in units

@@ -490,3 +490,28 @@ def test_long_rows_keep_the_second_term_of_fp32_weights():
     w = np.exp2(t - t.max(0) + 12)
     one = (w.astype(np.float16).astype(float).T @ vv) / w.sum(0)[:, None]
     assert (np.abs(one - ref[0, 0]) > tol[0, 0]).any()
+
+
+@pytest.mark.parametrize("dtype,size,huge,scale", [("bf16", 100, 60, None), ("f32", 100, 60, None), ("f16", 10, 127, 64.0)])
+@pytest.mark.parametrize("blocks", [slice(1, None, 2), slice(0, 3), slice(None)])
+@pytest.mark.parametrize("top_k", [0, 50])
+def test_zero_keys_of_a_huge_scale(dtype, size, huge, scale, blocks, top_k):
+    """Keys of zero score 0, although query and scale alone are too large for each other's product."""
+    def zero(rng, pools, table, n_slots, listed):
+        k, v, ks, vs = pools
+        ks *= np.float32(2.0 ** -size) / (64 if scale else 1)
+        for r in range(table.shape[0]):
+            at = table[r, blocks]
+            k[at[at >= 0]], ks[at[at >= 0]] = 0, 2.0 ** huge
+    check(dtype, 8, 2, 64, [370, 64, 3], mutate=zero, q_size=2.0 ** size, scale=scale, top_k=top_k)
+    check(dtype, 32, 1, 128, [370, 700], mutate=zero, q_size=2.0 ** size, scale=scale, top_k=top_k, rows=2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("top_k", [0, 50])
+def test_queries_as_small_as_the_scales_are_large(dtype, top_k):
+    """Moderate scores of queries near 2^-100 and keys of scales near the largest."""
+    def large(rng, pools, table, n_slots, listed):
+        pools[2] *= np.float32(2.0 ** 100)
+    check(dtype, 8, 2, 64, [370, 64, 3], mutate=large, q_size=2.0 ** -100, top_k=top_k)
+    check(dtype, 32, 1, 128, [370, 700], mutate=large, q_size=2.0 ** -100, top_k=top_k, rows=2)
