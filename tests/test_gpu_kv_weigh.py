@@ -125,6 +125,30 @@ def test_zero_keys_of_a_huge_scale():
     check("bf16", 8, 2, 64, [1, 1], [100, 5], seed=4, mutate=mutate)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("news,before", [([70, 1], [500, 5]), ([200, 40], [300, 64]), ([1, 1], [500, 5]), ([5, 2], [500, 64])])
+def test_queries_as_small_as_the_scales_are_large(dtype, news, before):
+    # moderate scores, although a score and its page's scale alone are too large for each other's product
+    def large(rng, k, ks, table, q, lse, weight):
+        q *= 2.0 ** -100
+        ks *= np.float32(2.0 ** 101)
+    check(dtype, 8, 2, 128, news, before, seed=5, mutate=large)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("news,before", [([200, 40], [300, 64]), ([1, 1], [500, 5]), ([5, 2], [500, 64])])
+def test_zero_keys_of_a_huge_scale_beside_others(dtype, news, before):
+    # (with rows that do not share a power of two, too)
+    def mutate(rng, k, ks, table, q, lse, weight):
+        q *= 2.0 ** 100
+        q[:2] *= 2.0 ** -30
+        ks *= np.float32(2.0 ** -100)
+        for r in range(table.shape[0]):
+            at = table[r, ::2]
+            k[at[at >= 0]], ks[at[at >= 0]] = 0, 2.0 ** 60
+    check(dtype, 8, 2, 128, news, before, seed=6, mutate=mutate)
+
+
 @pytest.mark.parametrize("R", [257, 1100])
 def test_very_many_requests(R):
     rng = np.random.default_rng(R)
