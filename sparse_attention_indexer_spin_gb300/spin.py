@@ -718,7 +718,7 @@ class PromptAttention:
         self.k, self.v = (torch.empty((n_tokens, cfg.kv_heads, cfg.head_dim), dtype=t, device=device) for _ in range(2))
         self.lse = torch.empty((n_tokens, cfg.n_heads), dtype=torch.float32, device=device)
 
-    def check(self, q, k, v, positions, new_start, max_new, n_before, block_table, status, weight):
+    def check(self, q, k, v, positions, new_start, max_new, n_before, block_table, status, weight, decay=1.0):
         """Refuses arguments that a step of run_prompt would refuse, without a launch."""
         cfg, dev, T = self.cfg, torch._C._cuda_getDevice(), q.shape[0]
         if T > self.n_tokens or not 0 <= max_new <= min(self.max_new, cfg.max_slots):
@@ -743,6 +743,8 @@ class PromptAttention:
             raise SpinError(2, "block_table holds %d slots a request, max_slots is %d" % (64 * block_table.shape[-1], cfg.max_slots))
         if weight is not None:
             _arg("weight", weight, torch.float32, (cfg.n_req, 64 * block_table.shape[-1]), dev)
+            if not math.isfinite(ctypes.c_float(decay).value):
+                raise SpinError(1, "decay is not finite")
         _status_arg(status, dev)
 
 
@@ -967,7 +969,7 @@ def run_prompt(core: PromptAttention, q, k, v, new_start, max_new, n_before, blo
     slots from n_before[r] on, whose pages are there (pages_reserve).  With positions int32 [T] queries and keys are rotated by
     core.rope first; with weight fp32 [R][64 bt] the attention weight that the slots get from these tokens is added to it, after
     its multiplication with decay.  Returns core.out[:T] and core.lse[:T]; the rows of tokens behind the last request stay."""
-    core.check(q, k, v, positions, new_start, max_new, n_before, block_table, status, weight)
+    core.check(q, k, v, positions, new_start, max_new, n_before, block_table, status, weight, decay)
     cfg, T = core.cfg, q.shape[0]
     out, lse = core.out[:T], core.lse[:T]
     with torch.cuda.stream(stream):

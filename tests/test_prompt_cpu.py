@@ -247,6 +247,26 @@ def test_prompt_run_refusals(spin_lib, monkeypatch):
         spin.PromptAttention(cfg, cache, -1, 4, device="cpu")
 
 
+@pytest.mark.parametrize("decay", [float("nan"), float("inf"), -float("inf"), 1e39, None])
+def test_prompt_run_refuses_a_decay_before_it_writes(spin_lib, monkeypatch, decay):
+    """The last step's argument is looked at before the first step; a decay that no step reads is not."""
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1)
+    called = []
+    for name in ("rope", "kv_append", "kv_prefill", "kv_weigh"):
+        monkeypatch.setattr(spin, name, lambda *a, name=name: called.append(name))
+    cfg = spin.make_kv_config(1, 64, 1, 2, 1, 16, "bf16")
+    core = spin.PromptAttention(cfg, spin.KvCache(2, 1, 16, device="cpu"), 4, 4, device="cpu")
+    q, kv = (torch.zeros((4, h, 16), dtype=torch.bfloat16) for h in (2, 1))
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)  # noqa: E731
+    call = lambda **kw: spin.run_prompt(core, q, kv, kv, i32(0, 4), 4, i32(0), i32(0)[None], None, **kw)  # noqa: E731
+    with pytest.raises((spin.SpinError, TypeError)):
+        call(weight=torch.zeros((1, 64)), decay=decay)
+    assert not called
+    call(decay=decay)
+    call(weight=torch.zeros((1, 64)), decay=-2.0)
+    assert called == ["kv_append", "kv_prefill"] * 2 + ["kv_weigh"]
+
+
 # ------------------------------------------------------------------------------------------- eviction
 
 def evict_call(code, word, **kw):
