@@ -721,6 +721,8 @@ class PromptAttention:
     def check(self, q, k, v, positions, new_start, max_new, n_before, block_table, status, weight, decay=1.0):
         """Refuses arguments that a step of run_prompt would refuse, without a launch."""
         cfg, dev, T = self.cfg, torch._C._cuda_getDevice(), q.shape[0]
+        if self.out.get_device() != dev:
+            raise SpinError(1, "the buffers are on %s, the current device is cuda:%d" % (self.out.device, dev))
         if T > self.n_tokens or not 0 <= max_new <= min(self.max_new, cfg.max_slots):
             raise SpinError(2, "%d tokens, %d of a request at most; there is room for %d and %d" % (
                 T, max_new, self.n_tokens, self.max_new))

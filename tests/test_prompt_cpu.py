@@ -267,6 +267,20 @@ def test_prompt_run_refuses_a_decay_before_it_writes(spin_lib, monkeypatch, deca
     assert called == ["kv_append", "kv_prefill"] * 2 + ["kv_weigh"]
 
 
+def test_prompt_run_refuses_buffers_elsewhere(spin_lib, monkeypatch):
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: -1)
+    cfg = spin.make_kv_config(1, 64, 1, 2, 1, 16, "bf16")
+    core = spin.PromptAttention(cfg, spin.KvCache(2, 1, 16, device="cpu"), 4, 4, device="cpu")
+    q, kv = (torch.zeros((4, h, 16), dtype=torch.bfloat16) for h in (2, 1))
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)  # noqa: E731
+    args = (q, kv, kv, None, i32(0, 4), 4, i32(0), i32(0)[None], None, None)
+    core.check(*args)
+    core.out = core.out.to("meta")      # (a device of another number)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda x: 1 if x.is_meta else -1)
+    with pytest.raises(spin.SpinError, match="buffers"):
+        core.check(*args)
+
+
 # ------------------------------------------------------------------------------------------- eviction
 
 def evict_call(code, word, **kw):
