@@ -522,8 +522,8 @@ def rope_frequencies(rot_dim, theta=10000.0, scaling=None, factor=1.0, original=
                 the pairs between; magnitude 0.1 ln(factor) + 1"""
     if rot_dim < 2 or rot_dim % 2:
         raise SpinError(1, "rot_dim %d must be even and at least 2" % rot_dim)
-    if not (theta > 0 and factor >= 1.0):
-        raise SpinError(1, "theta must be positive and factor at least 1")
+    if not (0 < theta < math.inf and 1.0 <= factor < math.inf):
+        raise SpinError(1, "theta must be positive and factor at least 1, both finite")
     i = torch.arange(0, rot_dim, 2, dtype=torch.float64) / rot_dim
     if scaling is None:
         if factor != 1.0:
@@ -534,12 +534,13 @@ def rope_frequencies(rot_dim, theta=10000.0, scaling=None, factor=1.0, original=
     if scaling == "base":
         return (theta * factor ** (rot_dim / max(1, rot_dim - 2))) ** -i, 1.0
     if scaling == "parts":
-        if original is None or not original > 0 or not fast > slow > 0 or theta == 1.0:
-            raise SpinError(1, "parts: original > 0, fast > slow > 0 and theta other than 1 needed")
+        if original is None or not 0 < original < math.inf or not fast > slow > 0 or theta <= 1.0:
+            raise SpinError(1, "parts: original > 0, fast > slow > 0 and theta above 1 needed")
         # the pair (a real number) that turns x times within the original context
         pair = lambda x: rot_dim * math.log(original / (2 * math.pi * x)) / (2 * math.log(theta))  # noqa: E731
         lo, hi = max(0, math.floor(pair(fast))), min(rot_dim - 1, math.ceil(pair(slow)))
         ramp = ((torch.arange(rot_dim // 2, dtype=torch.float64) - lo) / max(hi - lo, 1e-3)).clamp(0.0, 1.0)
+        ramp[max(0, math.ceil(pair(slow))):] = 1.0     # (the first pair too, where even that turns no more than `slow` times)
         f = theta ** -i
         return f * (1.0 - ramp) + f / factor * ramp, 0.1 * math.log(factor) + 1.0
     raise SpinError(1, "scaling must be None, linear, base or parts; got %r" % (scaling,))

@@ -130,6 +130,23 @@ def test_rope_frequencies():
             spin.rope_frequencies(**bad)
 
 
+@pytest.mark.parametrize("original,fast,slow", [(4, 32.0, 1.0), (6, 2.0, 1.0), (6.2, 32.0, 1.0), (100, 64.0, 16.0), (4096, 32.0, 1.0), (200, 64.0, 31.0)])
+def test_rope_frequencies_by_parts_at_the_ends(original, fast, slow):
+    """Pairs that turn `slow` times or less within the original context are divided, the first one among them."""
+    f, _ = spin.rope_frequencies(64, 1e4)
+    g, _ = spin.rope_frequencies(64, 1e4, "parts", 8.0, original=original, fast=fast, slow=slow)
+    turns = f * original / (2 * math.pi)
+    assert torch.allclose((g / f)[turns <= slow], torch.tensor(0.125, dtype=torch.float64), rtol=1e-14)
+    assert (g[turns >= fast] == f[turns >= fast]).all()
+
+
+def test_rope_frequencies_of_no_meaning():
+    for bad in (dict(theta=math.inf), dict(theta=math.nan), dict(scaling="linear", factor=math.inf), dict(scaling="base", factor=math.nan),
+                dict(theta=0.5, scaling="parts", factor=2.0, original=4096), dict(scaling="parts", factor=2.0, original=math.inf)):
+        with pytest.raises(spin.SpinError):
+            spin.rope_frequencies(8, **bad)
+
+
 def test_rope_turns():
     t = spin.rope_turns(torch.tensor([0.0, math.pi, 2 * math.pi, -math.pi / 2, 1.0], dtype=torch.float64), "cpu")
     u = [x % (1 << 64) for x in t.tolist()]
