@@ -443,6 +443,13 @@ spin_status_t spin_allocate_budgets(const float* miss, int32_t n_layers, int32_t
 spin_status_t spin_selftest_wait(int32_t mode, uint64_t limit_ns, uint32_t* status,
                                  uint64_t* elapsed_ns, spin_stream_t stream);
 
+/* The same for the wait whose limit (0 < limit_ns <= 1 s) begins anew while a counter moves, which a kernel uses where
+ * the work of others has no bound of its own: a second warp moves the counter `steps` times (0 .. 16), three quarters of
+ * the limit apart, and as long after the last time arrives (arrives = 1: the wait must succeed) or stays away (0: it must
+ * end one to two limits after the last move, with SPIN_STATUS_TIMEOUT). */
+spin_status_t spin_selftest_wait_moving(int32_t steps, int32_t arrives, uint64_t limit_ns, uint32_t* status,
+                                        uint64_t* elapsed_ns, spin_stream_t stream);
+
 /* spin_update_ema under SPIN_EXPLORE_BLOCK_AGE: also sets block_age[req][blk] = step + 1 for
  * every listed block inside the context (device, read-write; zero it at a reset).  The other
  * update entry points refuse BLOCK_AGE (SPIN_ERR_INVALID_ARG). */

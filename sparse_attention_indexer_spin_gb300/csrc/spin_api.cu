@@ -518,6 +518,19 @@ spin_status_t spin_selftest_wait(int32_t mode, uint64_t limit_ns, uint32_t* stat
                     "spin_selftest_wait");
 }
 
+spin_status_t spin_selftest_wait_moving(int32_t steps, int32_t arrives, uint64_t limit_ns, uint32_t* status,
+                                       uint64_t* elapsed_ns, spin_stream_t stream) {
+    g_err[0] = 0;
+    if (steps < 0 || steps > 16) return fail(SPIN_ERR_INVALID_ARG, "steps %d outside [0, 16]", steps);
+    if (arrives != 0 && arrives != 1) return fail(SPIN_ERR_INVALID_ARG, "arrives must be 0 or 1");
+    if (!status || !elapsed_ns) return fail(SPIN_ERR_INVALID_ARG, "status and elapsed_ns must be non-NULL");
+    if (limit_ns == 0 || limit_ns > 1000ull * 1000ull * 1000ull)
+        return fail(SPIN_ERR_INVALID_ARG, "limit_ns outside (0, 1 s]");
+    return launched(launch_wait_moving_selftest(steps, arrives, limit_ns, status,
+                                                reinterpret_cast<unsigned long long*>(elapsed_ns), (cudaStream_t)stream),
+                    "spin_selftest_wait_moving");
+}
+
 static spin_status_t check_kv(const spin_kv_config* c) {
     g_err[0] = 0;
     if (!c) return fail(SPIN_ERR_INVALID_ARG, "cfg is NULL");

@@ -312,6 +312,18 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     }
 }
 
+// The same for a wait that others' work may lengthen without bound: the limit begins anew as long as *progress moves.
+__device__ __forceinline__ bool mbar_wait_while(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                volatile uint32_t* progress, uint64_t limit_ns = kWaitLimitNs) {
+    for (uint32_t seen = *progress;;) {
+        if (mbar_wait(bar, parity, abort_flag, limit_ns)) return true;
+        if (abort_flag && *abort_flag) return false;
+        const uint32_t now = *progress;
+        if (now == seen) return false;
+        seen = now;
+    }
+}
+
 // Contiguous global -> shared copy by the bulk-copy (TMA) engine, completing on `bar`.
 // dst, src 16-byte aligned, bytes a multiple of 16.
 __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {

@@ -215,6 +215,8 @@ cudaError_t launch_pages_evict(const PageTable& t, const PageEvictArgs& a, cudaS
 // Self-test of the bounded mbarrier wait (spin_selftest.cu).
 cudaError_t launch_wait_selftest(int mode, uint64_t limit_ns, uint32_t* status, unsigned long long* elapsed_ns,
                                  cudaStream_t s);
+cudaError_t launch_wait_moving_selftest(int steps, int arrives, uint64_t limit_ns, uint32_t* status,
+                                        unsigned long long* elapsed_ns, cudaStream_t s);
 
 // Per-layer block budgets (host functions; spin_budget.cu).  Arguments are validated by the
 // C-ABI wrappers.

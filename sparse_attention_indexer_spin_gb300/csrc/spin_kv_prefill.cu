@@ -151,6 +151,7 @@ struct PfHdr {
     uint64_t fin;
     uint32_t tmem_base;
     int abort_flag;
+    uint32_t tiles;       // whose codes the converters have begun with: what moves while a job goes on
     int64_t into;
     int chunk;
     PfScale sc[kPfRing][2];
@@ -301,6 +302,7 @@ prefill_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_constant
         }
         mbar_init(&hdr->fin, 1);
         hdr->abort_flag = 0;
+        hdr->tiles = 0;
         fence_barrier_init();
     }
     {   // the chunk that this CTA's part begins in
@@ -774,6 +776,7 @@ prefill_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_constant
                     e.ratio = strange ? vs * ex2(-lv) : 1.0f;
                     e.live = mine >= 0;
                     e.odd = strange;
+                    if (ct == 0) *(volatile uint32_t*)&hdr->tiles = it + 1;
                     mbar_arrive(&hdr->scale[it % kPfRing]);
                 }
                 __syncwarp();
@@ -828,8 +831,13 @@ prefill_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_constant
         for (uint32_t n = 0;; ++n) {
             PfJob& job = hdr->job[n % kPfJobs];
             if (!wait(&hdr->jdone[n % kPfJobs], (n / kPfJobs) ^ 1u)) break;
-            // the outputs of the job before last are out: its list of NaN begins anew for this one
-            if (n >= 2 && !wait(&hdr->epi[n & 1], (n >> 1) - 1)) break;
+            // the outputs of the job before last are out: its list of NaN begins anew for this one.  All of a job may pass
+            // meanwhile (2^24 slots of 256 fp32 dimensions: 0.73 s at full clocks, near a wait's limit of 1 s), so that this
+            // wait's limit begins anew while tiles go on.
+            if (n >= 2 && !__all_sync(0xffffffffu, mbar_wait_while(&hdr->epi[n & 1], ((n >> 1) - 1) & 1u, &hdr->abort_flag, &hdr->tiles))) {
+                fail_wait();
+                break;
+            }
             for (int e = lane; e < D; e += 32) hdr->nan[n & 1][e] = 0x7fffffff;
             __syncwarp();
             if (lane == 0) {

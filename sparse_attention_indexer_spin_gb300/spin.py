@@ -180,6 +180,7 @@ def lib():
             "spin_pages_copy": [i32, i64, P, i32, P, ctypes.c_size_t, P, P],
             "spin_pages_compact": [i32, i64, P, i64, P, P, i32, P, P, ctypes.c_size_t, P, P],
             "spin_selftest_wait": [i32, u64, P, P, P],
+            "spin_selftest_wait_moving": [i32, i32, u64, P, P, P],
             "spin_miss_curve": [P, i32, i64, P, P, i32, i32, P],
             "spin_allocate_budgets": [P, i32, i32, i32, i32, P, P],
         }
@@ -259,6 +260,12 @@ def selftest_wait(mode, limit_ns, status, elapsed_ns, stream=None):
     """spin_selftest_wait: the library's bounded barrier wait, with no arrival (mode 0), the
     abort flag raised (1) or an arrival (2)."""
     _check(lib().spin_selftest_wait(int(mode), int(limit_ns), _ptr(status), _ptr(elapsed_ns), _stream(stream)))
+
+
+def selftest_wait_moving(steps, arrives, limit_ns, status, elapsed_ns, stream=None):
+    """spin_selftest_wait_moving: the wait whose limit begins anew while a counter moves; the counter moves `steps` times,
+    then the arrival comes (arrives true) or does not."""
+    _check(lib().spin_selftest_wait_moving(int(steps), int(arrives), int(limit_ns), _ptr(status), _ptr(elapsed_ns), _stream(stream)))
 
 
 def version() -> str:

@@ -67,3 +67,29 @@ def test_selftest_rejects_bad_arguments():
         spin.selftest_wait(3, MS, status, elapsed)
     with pytest.raises(spin.SpinError):
         spin.selftest_wait(0, 0, status, elapsed)
+
+
+def _run_moving(steps, arrives, limit_ns):
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    elapsed = torch.zeros(1, dtype=torch.int64, device="cuda")
+    spin.selftest_wait_moving(steps, arrives, limit_ns, status, elapsed)
+    torch.cuda.synchronize()
+    return int(status.item()), int(elapsed.item())
+
+
+@pytest.mark.parametrize("steps", [0, 1, 4, 16])
+def test_a_limit_that_begins_anew_while_a_counter_moves(steps):
+    """A counter that moves every 15 ms keeps a wait of 20 ms alive; once it rests, the wait ends."""
+    status, ns = _run_moving(steps, True, 20 * MS)
+    assert status == 0 and 15 * (steps + 1) * MS <= ns < 15 * (steps + 1) * MS + 200 * MS
+    status, ns = _run_moving(steps, False, 20 * MS)
+    assert status & spin.STATUS_BITS["TIMEOUT"]
+    assert (15 * steps + (20 if steps == 0 else 0)) * MS <= ns < (15 * steps + 40) * MS + 200 * MS
+
+
+def test_moving_selftest_rejects_bad_arguments():
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    elapsed = torch.zeros(1, dtype=torch.int64, device="cuda")
+    for steps, arrives, limit in ((-1, 0, MS), (17, 0, MS), (1, 2, MS), (1, 0, 0), (1, 0, 1001 * MS)):
+        with pytest.raises(spin.SpinError):
+            spin.selftest_wait_moving(steps, arrives, limit, status, elapsed)
