@@ -591,7 +591,9 @@ spin_status_t spin_rope(const spin_rope_config* cfg, const spin_rope_rows* rows,
  * new_start[r+1]-1 of q ([n_tokens][n_heads][head_dim]) are its slots n_before[r], n_before[r]+1,
  * ..., whose keys and values the cache holds already (spin_kv_append), and token t sees the slots up
  * to its own, i <= n_before[r] + t.  Formulas, types, layouts and precision are spin_kv_attend's (but that a weight far
- * below its row's largest is off by up to 2^-34 of that, not 2^-37); out
+ * below its row's largest is off by up to 2^-34 of that, not 2^-37, and that sums are cut off by 2^-24 of themselves on average
+ * at each addition of 16 slots (two for F32), over stretches of at most 49152 slots (F32: 6144), which are then rounded to
+ * nearest); out
  * [n_tokens][n_heads][head_dim] and lse [n_tokens][n_heads] (may be NULL).  A token that sees no slot
  * with a page gets out = 0 and lse = -inf.  Tokens of no request keep their outputs.
  * max_new: the largest count of new tokens of a request (sizes the launch).  n_tokens * n_heads < 2^31,

@@ -49,6 +49,10 @@ constexpr int kPfJobs = 4;         // jobs worked out ahead
 constexpr int kPfJobUnits = 7;
 constexpr int kPfMinCost = 4;      // cost a CTA takes at least, in tiles of slots
 constexpr int kPfMostSms = 512;
+// Slots whose products tensor memory adds up (half as many more at a job's end) before the sums leave it for a record that is
+// added to with rounding to nearest.  Tensor memory's own additions, one for 16 slots (two for fp32), cut off: 2^-24 of the sum
+// each on average, all in one direction.  Without this a CTA's 2^20 slots of one sign came out 0.1 % short, 2^24 7 %.
+__host__ __device__ constexpr int pf_fold(bool split) { return split ? 4096 : 32768; }
 constexpr float kPfTop = 9.0f;     // log2 of the largest weight when the reference is set: 64 of them are within f16
 constexpr float kPfSlack = 6.0f;   // a maximum may exceed that by this much before the reference moves
 
@@ -62,6 +66,7 @@ template <typename T, int D, int NQ> struct PfShape {
     static constexpr uint32_t Q_BYTES = NQ * Q_TILE * (SPLIT ? 2 : 1);
     static constexpr uint32_t KV = BN * D * 2;                  // keys, or values, of a stage
     static constexpr uint32_t COLS = NQ * (SB * BN + D) > 256 ? 512 : 256;
+    static constexpr int FOLD = pf_fold(SPLIT) / BN;            // tiles between two of those, a power of two
     static constexpr uint32_t HDR = 4096;
     static constexpr uint32_t BYTES = HDR + Q_BYTES + NST * 2 * KV + 1024;   // (slack for 1024-byte alignment)
 };
@@ -74,6 +79,7 @@ struct PfPlan {
     int2* tokens;       // {first token, count} of the chunk's request
     int4* owner;        // per CTA: the divided job that it begins: {chunk, key head, pieces, 0}
     float* rec;         // two records per CTA: rows x D sums, then (reference, sum) of each row
+    float* fold;        // per CTA: D x rows sums that left tensor memory (where contexts are long enough)
     int* base;          // [requests + 1] chunks before
     int most;           // chunks that fit
     int ranks;          // CTAs that may work
@@ -450,7 +456,28 @@ prefill_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_constant
             float mx = ninf, l = 0.0f;
             bool far = false, primed = false;   // a reference of kAtFar or more; every row of the warp has one
             const int u0 = job.u0, u1 = job.u1;
+            float held = ninf;    // the reference of the sums that left
             for (int u = u0; u < u1; ++u, ++it) {
+                if (((u - u0) & (S::FOLD - 1)) == 0 && u != u0 && u1 - u >= S::FOLD / 2) {
+                    if (!(ok = wait(&hdr->pvdone[i][(it - 1) & 1], (it - 1) >> 1))) break;
+                    tc_fence_after();
+                    float* to = plan.fold + (int64_t)blockIdx.x * ROWS * D + i * kPfRows + m;
+                    const bool again = u - u0 > S::FOLD;
+                    const float f = mx == ninf ? 1.0f : ex2(held - mx);
+#pragma unroll 1
+                    for (int c = 0; c < d; c += 16, to += 16 * ROWS) {
+                        float o[16], y[16];
+                        const uint32_t none[16] = {};
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) y[x] = again ? to[x * ROWS] : 0.0f;
+                        tm_ld16(tO + c, o);
+                        tm_st16(tO + c, none);
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) to[x * ROWS] = again ? fmaf(y[x], f, o[x]) : o[x];
+                    }
+                    tm_wait_st();
+                    held = mx;
+                }
                 if (!(ok = wait(&hdr->scale[it % kPfRing], it / kPfRing) && wait(&hdr->sfull[i][it & 1], it >> 1))) break;
                 tc_fence_after();
                 bool broke = false;
@@ -507,15 +534,16 @@ prefill_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_constant
                     tm_ld32(tS + 32, s + 32);
                     tm_wait32(s);
                     tm_wait32(s + 32);
-                    if (fabsf(c) == __uint_as_float(0x7f800000u)) {
-                        // an overflow of the factors' product is no score's: keys of zero score 0 whatever their scale
+                    // an overflow of the factors' product is no score's (keys of zero score 0 whatever their scale): then one by one
+                    const bool huge = fabsf(c) == __uint_as_float(0x7f800000u);
+                    if (border || huge) {
+                        if (huge) c = qs;
+#pragma unroll 1
+                        for (int both = huge; both >= 0; --both) {
+                            const float a = both ? sc.ks : c;
 #pragma unroll
-                        for (int x = 0; x < kBlock; ++x) s[x] *= sc.ks;
-                        c = qs;
-                    }
-                    if (border) {
-#pragma unroll
-                        for (int x = 0; x < kBlock; ++x) s[x] = x < n ? s[x] * c : ninf;
+                            for (int x = 0; x < kBlock; ++x) s[x] = x < n ? s[x] * a : ninf;
+                        }
                         c = 1.0f;
                     }
                     float top = ninf;
@@ -554,13 +582,7 @@ prefill_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_constant
 #pragma unroll 1
                                 for (int c = 0; c < D; c += 16) {
                                     float o[16];
-                                    asm volatile(
-                                        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-                                        "%12, %13, %14, %15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
-                                        : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7]),
-                                          "=f"(o[8]), "=f"(o[9]), "=f"(o[10]), "=f"(o[11]), "=f"(o[12]), "=f"(o[13]), "=f"(o[14]), "=f"(o[15])
-                                        : "r"(tO + c)
-                                        : "memory");
+                                    tm_ld16(tO + c, o);
                                     uint32_t w[16];
 #pragma unroll
                                     for (int x = 0; x < 16; ++x) w[x] = __float_as_uint(o[x] * f);
@@ -617,6 +639,9 @@ prefill_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_constant
             // Through the queries' place (their products have ended), a row's line by its thread, then the warp's lines
             // one after another, 16 bytes a lane; sums of a piece in 32 bits, half a row at a time where a line holds that.
             const int rounds = whole || SPLIT ? 1 : 2, cols = D / rounds;
+            const bool folded = u1 - u0 >= S::FOLD + S::FOLD / 2;
+            const float* left = plan.fold + (int64_t)blockIdx.x * ROWS * D + at_row;
+            held = mx == ninf ? 1.0f : ex2(held - mx);    // the factor of the sums that left
 #pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += cols) {
 #pragma unroll 1
@@ -625,6 +650,17 @@ prefill_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_constant
                     __syncwarp();
                     tm_ld32(tO + c, o);
                     tm_wait32(o);
+                    if (folded) {
+#pragma unroll
+                        for (int h = 0; h < 32; h += 16) {
+                            if (c + h >= d) break;
+                            float y[16];
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) y[x] = left[(c + h + x) * ROWS];
+#pragma unroll
+                            for (int x = 0; x < 16; ++x) o[h + x] = fmaf(y[x], held, o[h + x]);
+                        }
+                    }
 #pragma unroll
                     for (int x = 0; x < 32; x += 4) {
                         const int4 first = nan[(c + x) / 4];
@@ -1043,6 +1079,8 @@ static size_t pf_layout(const spin_kv_config& cfg, int64_t n_tokens, void* ws, P
     q.owner = reinterpret_cast<int4*>(take(sms * sizeof(int4)));
     q.base = reinterpret_cast<int*>(take(((size_t)cfg.n_req + 1) * 4));
     q.rec = reinterpret_cast<float*>(take(sms * 2 * 2 * kPfRows * ((size_t)pf_dim(cfg.head_dim) + 2) * sizeof(float)));
+    const bool folds = cfg.max_slots > pf_fold(cfg.dtype == SPIN_DTYPE_F32);
+    q.fold = reinterpret_cast<float*>(take(folds ? sms * 2 * kPfRows * (size_t)pf_dim(cfg.head_dim) * sizeof(float) : 0));
     q.most = (int)n;
     q.ranks = (int)sms;
     if (p) *p = q;
