@@ -237,7 +237,7 @@ weigh_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_constant__
             __syncthreads();
 
             // ---- weights
-            float sum[2];
+            float sum[2] = {0.0f, 0.0f};
             auto head = [&](uint32_t stage, int u, int g) {
                 cp_wait<AHEAD - 1>();
                 uint32_t kf[C][4][4];                     // [64 dims][step][fragment]

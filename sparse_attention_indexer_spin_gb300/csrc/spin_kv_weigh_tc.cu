@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kWtRowThreads) weigh_tc_rows_kernel(spin_kv_co
             }
         }
         __syncthreads();
-        const bool same = s_high - s_low <= 8 || s_low == 0x7fffffff;
+        const bool same = s_low == 0x7fffffff || s_high - s_low <= 8;   // (s_low as it was set: only zeros)
         const int common = s_low == 0x7fffffff ? 0 : s_high;
 #pragma unroll
         for (int n = 0; n < N; ++n) {
