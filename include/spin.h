@@ -616,8 +616,11 @@ spin_status_t spin_kv_prefill(const spin_kv_config* cfg, const void* q, int64_t 
  * spin_kv_prefill; a decoded token is a request's only one), summed over tokens and heads:
  *   weight[r][i] <- decay weight[r][i] + sum_{t, h: i <= n_before[r] + t} exp(s_{t,h,i} - lse[t][h])
  * for the slots i < n_before[r] + its count, where slots from n_before[r] on start from 0.
- * weight float [R][64 bt_stride]; lse is what spin_kv_attend or spin_kv_prefill returned for these
- * queries; a row of lse = -inf saw nothing and adds nothing.  Requests without new tokens, slots
+ * weight float [R][64 bt_stride]; lse is what spin_kv_prefill, or spin_kv_attend over whole contexts,
+ * returned for these queries (over a list of slots it is the list's own: the slots outside would get
+ * weight that they did not have); a row of lse = -inf saw nothing and adds nothing.  An array is one
+ * layer's: a second layer's call would drop what the first gave the new slots.  Layers on one table
+ * keep one each and are added up for an eviction.  Requests without new tokens, slots
  * behind the context and slots without a page (BAD_PAGE) keep their weight.  decay: finite (0: the
  * weight from before is not read).
  * Scores have spin_kv_attend's precision (with many rows, a row whose largest query value is far below those of its
@@ -705,8 +708,10 @@ spin_status_t spin_pages_copy(int32_t n_req, int64_t n_pages, const spin_page_po
  * table entries (pages reserved behind the context move down too), weight_out (same shape; slots behind
  * the context get 0), and n_slots[r] loses 64 for every block that went; pages lose a reference.
  * The slots' new places are positions in the cache only: cached keys keep the rotation that they have.
- * kept int32 [R][bt_stride]: the blocks that stayed, ascending, -1 behind them (what moves other arrays
- * along).  weight_out must not overlap weight.  n_first >= 0, n_last >= 1.
+ * kept int32 [R][bt_stride]: the blocks that stayed, ascending, -1 behind them.  All else that goes by a
+ * request's slots or blocks has to follow it, or to begin anew: other layers' weights, and the indexer's
+ * V, D, Vmax, block ages and top-K hint, which spin_init_state and spin_init_topk_hint of the request
+ * reset (its next selection is dense, over what stayed).  weight_out must not overlap weight.  n_first >= 0, n_last >= 1.
  * Checked on the device: n_slots outside [0, 64 bt_stride] (BAD_N: the request stays as it is, its kept is
  * -1), table entries outside [-1, n_pages) (BAD_PAGE, treated as -1) and BAD_REF as in spin_pages_free.
  * workspace: spin_pages_evict_workspace_size bytes, 256-byte aligned, uninitialised, not shared by calls that may

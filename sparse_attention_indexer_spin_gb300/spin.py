@@ -637,7 +637,8 @@ def kv_prefill(cfg, q, new_start, max_new, n_before, k, v, k_scale, v_scale, blo
 def kv_weigh(cfg, q, lse, new_start, max_new, n_before, k, k_scale, block_table, decay, weight, workspace, status,
              stream=None):
     """spin_kv_weigh: adds the attention weight that the cached slots get from the tokens q (as in kv_prefill) to
-    weight fp32 [R][64 bt], after multiplying that by decay; lse fp32 [T][n_heads] as the attention returned it."""
+    weight fp32 [R][64 bt] (a layer's own), after multiplying that by decay; lse fp32 [T][n_heads] as the attention over
+    whole contexts returned it."""
     dev = torch._C._cuda_getDevice()
     ws, ws_bytes = _workspace_arg(workspace, dev)
     n, bt = k.shape[0], block_table.shape[-1]
@@ -712,7 +713,8 @@ class PromptAttention:
     """The attention of prompts' chunks, with its buffers for up to n_tokens tokens a call, max_new of one request: rotated
     queries and keys, out [T][n_heads][d], lse [T][n_heads] and the workspaces.  rope: a SpinRopeConfig of the cache's
     head_dim and type, with its turns; None: queries and keys come as they are to be used.  Chunks that may run at the same
-    time (on other streams) need one each; the layers of a model, one after the other, can share one by way of `cache`."""
+    time (on other streams) need one each; the layers of a model, one after the other, can share one by way of `cache` (but
+    not a weight array: see kv_weigh)."""
 
     def __init__(self, cfg: SpinKvConfig, cache: KvCache, n_tokens: int, max_new: int, rope: Optional[SpinRopeConfig] = None,
                  turns=None, device="cuda"):
@@ -870,8 +872,9 @@ def pages_evict_workspace(n_req: int, blocks: int, device="cuda"):
 def pages_evict(block_table, n_slots, weight, weight_out, keep_blocks, n_first, n_last, ref, kept, workspace, status,
                 stream=None):
     """spin_pages_evict: request r is cut down to keep_blocks[r] blocks (< 0: left as it is), the first n_first, the
-    newest n_last and the heaviest others by weight fp32 [R][64 bt] (kv_weigh's); weight_out takes the weights in
-    their new places, kept int32 [R][bt] the blocks that stayed."""
+    newest n_last and the heaviest others by weight fp32 [R][64 bt] (kv_weigh's; of layers on one table, their sum);
+    weight_out takes the weights in their new places, kept int32 [R][bt] the blocks that stayed.  A request's other arrays
+    by slots or blocks follow that, or are reset: the indexer's by init_state and TopkHint.reset."""
     R, bt, n_pages = _table_shape(block_table, ref)
     dev = torch._C._cuda_getDevice()
     ws, ws_bytes = _workspace_arg(workspace, dev)

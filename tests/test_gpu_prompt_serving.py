@@ -7,6 +7,7 @@ import torch
 import _kv
 from oracle import kv as o
 from sparse_attention_indexer_spin_gb300 import spin
+from sparse_attention_indexer_spin_gb300 import synthetic as syn
 
 pytestmark = pytest.mark.gpu
 H, KVH, D, PAGES, W = 16, 2, 64, 40, 12
@@ -257,3 +258,48 @@ def test_refused_chunks_launch_nothing():
         assert torch.equal(x, y)
     with pytest.raises(spin.SpinError):
         spin.PromptAttention(loop.cfg, loop.cache, 4, 4, spin.make_rope_config(128, "bf16"), loop.core.turns)
+
+
+@pytest.mark.parametrize("hinted", [False, True])
+def test_the_indexer_after_an_eviction(hinted):
+    """Requests that lost blocks have their state reset: the next step selects all that stayed and scores it as a state does
+    that never saw what left; the request that kept its blocks goes on as it was."""
+    wl = syn.CONFIGS["pr1"].replace(steps=6, n_layers=1, n_req=3, n0=900, top_k=64)
+    inp = syn.SyntheticInputs(wl, "cuda")
+    cfg = spin.make_config(**wl.config_fields())
+    R, width = wl.n_req, inp.block_table.shape[1]
+    states = [spin.LayerState(cfg) for _ in range(2)]
+    bufs = [spin.StepBuffers(cfg) for _ in range(2)]
+    hints = [spin.TopkHint(cfg) if hinted else None for _ in range(2)]
+
+    def step(i, n):
+        spin.run_step(cfg, states[i], bufs[i], q, w, inp.k_pool[0], inp.k_scale[0], inp.n_pages, table, n, qp, n_step, 0, hint=hints[i])
+
+    table = inp.block_table.clone()
+    for n_step in range(3):
+        q, w, qp = inp.step_inputs()
+        step(0, inp.n_slots)
+        inp.advance(n_step)
+    q, w, qp = inp.step_inputs()
+    n = inp.n_slots.clone()
+    blocks = (n + 63) // 64
+    ref = torch.bincount(table[table >= 0].long(), minlength=inp.n_pages).to(torch.int32)
+    weight = torch.rand((R, 64 * width), device="cuda")
+    left, kept, status = torch.empty_like(weight), torch.empty_like(table), i32([0])
+    spin.pages_evict(table, n, weight, left, i32([int(blocks[0]) - 5, -1, 3]), 1, 1, ref, kept, spin.pages_evict_workspace(R, width), status)
+    assert int(n[0]) == int(inp.n_slots[0]) - 5 * 64 and int(status.item()) == 0
+    for r in (0, 2):
+        spin.init_state(cfg, *(getattr(states[0], x) for x in ("V", "D", "Vmax", "warm")), r)
+        if hinted:
+            hints[0].reset(r)
+    qp, n_step = n - 1, 3                          # (a query stands in its slot)
+    step(0, n)
+    step(1, n)                                     # a state that is new for every request
+    torch.cuda.synchronize()
+    assert int(bufs[0].status.item()) == 0 and int(bufs[1].status.item()) == 0
+    for r in (0, 2):
+        m = (int(n[r]) + 63) // 64
+        assert int(bufs[0].n_blocks[r, 0]) == m and bufs[0].blocks[r, 0, :m].tolist() == list(range(m))
+        for x, y in ((bufs[0].topk, bufs[1].topk), *((getattr(states[0], x), getattr(states[1], x)) for x in ("V", "D", "Vmax", "warm"))):
+            assert torch.equal(x[r], y[r])
+    assert int(bufs[0].n_blocks[1, 0]) < int(bufs[1].n_blocks[1, 0])      # (warm: it selects)
