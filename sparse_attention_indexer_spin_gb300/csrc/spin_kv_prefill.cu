@@ -26,15 +26,17 @@
 // cycle and quarter, packing, tensor memory), and the last page's product has to end before the next scores may overwrite the
 // weights (258 and 300).  With two row tiles all of tensor memory is taken (scores 2 x 128 columns, sums 2 x 128), so
 // that scores cannot be a tile ahead.  How the issuing loop is laid out counts: with the row tiles unrolled 951 -> 857 us at
-// 2048 tokens behind 32768 slots (prompts 145 -> 152).  Slower there (from 951): the next scores page by page (1357:
+// 2048 tokens behind 32768 slots (ragged prompts 145 -> 152: a loop twice as long, whose code is fetched cold).  Slower there (from 951): the next scores page by page (1357:
 // 128 x 64 x 16 takes 48 cycles, not 32, and the issuing thread waits for room after four instructions); eight warps a row
 // tile, half a tile's slots each (1388: 80 registers a thread, and what does not fit comes from L2, as 201 KB of shared
 // memory leave little first-level cache); the second page's scores loaded while the first page's weights are stored (1075: the
-// page's code twice).  Leaving out a row tile without rows gained nothing with this loop (938).
-// Measured (bf16, 32 heads on 8 of 128): 2048 tokens behind 32768 slots 858 us, 1.32 PFLOP/s (0.68 of the measured
-// product rate); 8 ragged prompts of 100 to 2048 tokens 155 us, 0.40 PFLOP/s: short jobs, whose queries, first scores and
+// page's code twice).  Leaving out row tiles without a row: turns 269 -> 256, prompts 145 -> 160 in the loop before; in this one
+// the long chunk, which has no such tile, 857 -> 938.  No instance spills a register; the code of a job's start and end is fetched cold, and what is
+// added there shows in short jobs (prompts 157 -> 161 us with the sums that leave tensor memory and the second factor of zero keys).
+// Measured (bf16, 32 heads on 8 of 128): 2048 tokens behind 32768 slots 849 us, 1.34 PFLOP/s (0.69 of the measured
+// product rate); 8 ragged prompts of 100 to 2048 tokens 161 us, 0.39 PFLOP/s: short jobs, whose queries, first scores and
 // outputs nothing overlaps, on the diagonal, where half a tile's products are masked.  16 turns of 5 to 32 tokens behind up to
-// 32000 slots (f16, 64 heads on 8) 242 us, 0.51 PFLOP/s counted in rows that are there: row tiles are partly filled.
+// 32000 slots (f16, 64 heads on 8) 238 us, 0.52 PFLOP/s counted in rows that are there: row tiles are partly filled.
 #include "spin_kv_chunk.cuh"
 #include "spin_kv_tc.cuh"
 
@@ -42,12 +44,15 @@ namespace spin {
 
 constexpr int kPfRows = 128;       // rows of a row tile: the lanes of tensor memory
 constexpr int kPfRing = 8;         // tiles whose scales are kept (see kempty)
-constexpr int kPfThreads = 512;    // 16 warps: four for each row tile, one issuer, the rest converters
+constexpr int kPfThreads = 512;    // 16 warps: four for each row tile, one planner, one issuer, the rest converters
 constexpr int kPfIssuer = kPfThreads / 32 - 1, kPfPlanner = kPfIssuer - 1;
 constexpr int kPfJobs = 4;         // jobs worked out ahead
-// What starting a job costs, in tiles of slots (prompts, turns: 2 161, 276 us; 4 151, 251; 5 154, 247; 7 155, 242).
+// What starting a job costs, in tiles of slots: one value for all shapes (prompts of many short jobs, turns on long contexts:
+// 2 161, 276 us; 4 151, 251; 5 154, 247; 7 155, 242).
 constexpr int kPfJobUnits = 7;
-constexpr int kPfMinCost = 4;      // cost a CTA takes at least, in tiles of slots
+// Cost a CTA takes at least, in tiles of slots.  Less than a job's start: in small calls a part may lie within one and hold no tile
+// (its CTA works out no job and leaves).
+constexpr int kPfMinCost = 4;
 constexpr int kPfMostSms = 512;
 // Slots whose products tensor memory adds up (half as many more at a job's end) before the sums leave it for a record that is
 // added to with rounding to nearest.  Tensor memory's own additions, one for 16 slots (two for fp32), cut off: 2^-24 of the sum
@@ -274,7 +279,7 @@ prefill_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_constant
     // ------------------------------------------------------------------------------ set-up
     const int n_chunks = (int)plan.head[0];
     const int64_t total = plan.head[1];
-    if ((int64_t)blockIdx.x >= PfWalk::pf_ranks(plan, total)) return;   // (all CTAs from here on have some work)
+    if ((int64_t)blockIdx.x >= PfWalk::pf_ranks(plan, total)) return;   // (the CTAs from here on have no part)
     if (wid == kPfIssuer) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&hdr->tmem_base)),
                      "r"(S::COLS)

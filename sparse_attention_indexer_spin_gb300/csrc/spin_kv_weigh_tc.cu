@@ -20,9 +20,9 @@
 // from shared memory (a value that all lanes read costs it as much as 32 of their own, so rows that share a power of two spare
 // half), exponentials, sums, one behind the other.  The exponentials' pipe is 31 % active, the tensor pipe 31 %, issue 32 %.
 // Four groups (80 registers, 130 us), units of 256 slots (129) and loads of the next 32 columns ahead (135: registers that
-// do not fit go to L2) were slower.
-// Measured (32 heads on 8 of 128, bf16): 1024 tokens behind 8192 slots 116 us, 0.63 PFLOP/s and 0.29 10^12 weights a second;
-// 4 x 32 tokens behind up to 32000 slots (f16, 64 heads on 8) 82 us, 0.41 PFLOP/s.
+// do not fit go to L2) were slower.  (32 bytes a thread are spilled as it is.)
+// Measured (32 heads on 8 of 128, bf16): 1024 tokens behind 8192 slots 116 us, 0.63 PFLOP/s and 2.5 10^12 weights a second;
+// 4 x 32 tokens behind up to 32000 slots (f16, 64 heads on 8) 84 us, 0.40 PFLOP/s.
 #include "spin_kv_tc.cuh"
 
 namespace spin {

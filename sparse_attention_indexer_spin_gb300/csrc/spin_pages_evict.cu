@@ -9,7 +9,7 @@
 // Memory bounds it: each weight is read (those that stay twice) and written once.  A cluster of up to eight CTAs takes a
 // request where its table is not too wide: one launch, all of them reading and moving weights and the first choosing.  Wider
 // tables take three launches, their weights read and moved by the whole GPU.
-// 96 requests of 20000 to 131072 slots cut to a third (75 MB): 27 us, 2.8 TB/s; by three launches 38.  What is left to the
+// 96 requests of 20000 to 131072 slots cut to a third (75 MB): 30 us, 2.5 TB/s; by three launches 38.  What is left to the
 // copy rate (11 us) is the chain within a request: its weights, the choice by one CTA, the move.  8 requests of up to 2000
 // slots: 6 us.
 #include "spin_common.cuh"

@@ -36,7 +36,8 @@ template <typename T, int V> struct alignas(V * sizeof(T)) RopeVec {
 // a pair, two values).  `copies`: the values outside the rotated ones are copied too.  A thread's first item is on
 // its way while the angles are worked out.  Eight CTAs an SM, where registers allow (5000 tokens of 17 fp32 heads 24 us,
 // 28 with six); two items ahead took 94 us instead of 65 on 16384 tokens of 40 16-bit heads, CTAs that stay and take
-// token after token 69 to 97.
+// token after token 69 to 97.  These bounds spill a few words a thread (bf16 halves 16 bytes stored and 48 loaded, the others 12 at
+// most), which the times include.
 template <typename T, int V, bool HALF>
 __global__ void __launch_bounds__(kRopeThreads, HALF && V == 8 ? 6 : 8) rope_kernel(spin_rope_config cfg, RopeArgs a, int copies, int heads) {
     pdl_begin();
