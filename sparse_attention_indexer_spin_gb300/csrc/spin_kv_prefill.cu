@@ -32,11 +32,11 @@
 // memory leave little first-level cache); the second page's scores loaded while the first page's weights are stored (1075: the
 // page's code twice).  Leaving out row tiles without a row: turns 269 -> 256, prompts 145 -> 160 in the loop before; in this one
 // the long chunk, which has no such tile, 857 -> 938.  No instance spills a register; the code of a job's start and end is fetched cold, and what is
-// added there shows in short jobs (prompts 157 -> 161 us with the sums that leave tensor memory and the second factor of zero keys).
-// Measured (bf16, 32 heads on 8 of 128): 2048 tokens behind 32768 slots 849 us, 1.34 PFLOP/s (0.69 of the measured
-// product rate); 8 ragged prompts of 100 to 2048 tokens 161 us, 0.39 PFLOP/s: short jobs, whose queries, first scores and
+// added there shows in short jobs (prompts 157 -> 160 us with the sums that leave tensor memory and the second factor of zero keys).
+// Measured (bf16, 32 heads on 8 of 128): 2048 tokens behind 32768 slots 855 us, 1.33 PFLOP/s (0.68 of the measured
+// product rate); 8 ragged prompts of 100 to 2048 tokens 160 us, 0.39 PFLOP/s: short jobs, whose queries, first scores and
 // outputs nothing overlaps, on the diagonal, where half a tile's products are masked.  16 turns of 5 to 32 tokens behind up to
-// 32000 slots (f16, 64 heads on 8) 238 us, 0.52 PFLOP/s counted in rows that are there: row tiles are partly filled.
+// 32000 slots (f16, 64 heads on 8) 239 us, 0.52 PFLOP/s counted in rows that are there: row tiles are partly filled.
 #include "spin_kv_chunk.cuh"
 #include "spin_kv_tc.cuh"
 
@@ -259,6 +259,24 @@ template <bool SPLIT> __device__ __forceinline__ void store_weights(uint32_t tS,
     }
 }
 
+// A row's sums leave tensor memory for the record (`again`: which has some, under factor f).  Out of line, and the loop over
+// tiles inside one over stretches: with this code in the loop a single row tile took 4 to 7 % longer for every tile (one token
+// on 2^20 slots a CTA, bf16: 9.8 ms without it, 10.5 in the loop, 10.1 here; fp32, eight times as often: 13.7, 15.0, 14.7).
+template <int ROWS> __device__ __noinline__ void fold_sums(uint32_t tO, int d, float* to, bool again, float f) {
+#pragma unroll 1
+    for (int c = 0; c < d; c += 16, to += 16 * ROWS) {
+        float o[16], y[16];
+        const uint32_t none[16] = {};
+#pragma unroll
+        for (int x = 0; x < 16; ++x) y[x] = again ? to[x * ROWS] : 0.0f;
+        tm_ld16(tO + c, o);
+        tm_st16(tO + c, none);
+#pragma unroll
+        for (int x = 0; x < 16; ++x) to[x * ROWS] = again ? fmaf(y[x], f, o[x]) : o[x];
+    }
+    tm_wait_st();
+}
+
 // ---------------------------------------------------------------------------- the kernel
 template <typename T, int D, int NQ>
 __global__ void __launch_bounds__(kPfThreads, 1)
@@ -462,173 +480,165 @@ prefill_kernel(const __grid_constant__ spin_kv_config cfg, const __grid_constant
             bool far = false, primed = false;   // a reference of kAtFar or more; every row of the warp has one
             const int u0 = job.u0, u1 = job.u1;
             float held = ninf;    // the reference of the sums that left
-            for (int u = u0; u < u1; ++u, ++it) {
-                if (((u - u0) & (S::FOLD - 1)) == 0 && u != u0 && u1 - u >= S::FOLD / 2) {
+            for (int u = u0, stop = u0; stop < u1;) {
+                if (u != u0) {
+                    // the sums so far leave tensor memory
                     if (!(ok = wait(&hdr->pvdone[i][(it - 1) & 1], (it - 1) >> 1))) break;
                     tc_fence_after();
-                    float* to = plan.fold + (int64_t)blockIdx.x * ROWS * D + i * kPfRows + m;
-                    const bool again = u - u0 > S::FOLD;
-                    const float f = mx == ninf ? 1.0f : ex2(held - mx);
-#pragma unroll 1
-                    for (int c = 0; c < d; c += 16, to += 16 * ROWS) {
-                        float o[16], y[16];
-                        const uint32_t none[16] = {};
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) y[x] = again ? to[x * ROWS] : 0.0f;
-                        tm_ld16(tO + c, o);
-                        tm_st16(tO + c, none);
-#pragma unroll
-                        for (int x = 0; x < 16; ++x) to[x * ROWS] = again ? fmaf(y[x], f, o[x]) : o[x];
-                    }
-                    tm_wait_st();
+                    fold_sums<ROWS>(tO, d, plan.fold + (int64_t)blockIdx.x * ROWS * D + i * kPfRows + m, u - u0 > S::FOLD,
+                                    mx == ninf ? 1.0f : ex2(held - mx));
                     held = mx;
                 }
-                if (!(ok = wait(&hdr->scale[it % kPfRing], it / kPfRing) && wait(&hdr->sfull[i][it & 1], it >> 1))) break;
-                tc_fence_after();
-                bool broke = false;
+                stop = u1 - u >= S::FOLD + S::FOLD / 2 ? u + S::FOLD : u1;
+                for (; u < stop; ++u, ++it) {
+                    if (!(ok = wait(&hdr->scale[it % kPfRing], it / kPfRing) && wait(&hdr->sfull[i][it & 1], it >> 1))) break;
+                    tc_fence_after();
+                    bool broke = false;
 #pragma unroll 1
-                for (int h = 0; h < HALVES; ++h) {
-                    const uint32_t tS = lanes + (uint32_t)((SB * i + it % SB) * BN + kBlock * h);
-                    const PfScale& sc = hdr->sc[it % kPfRing][h];
-                    const int slot0 = u * BN + kBlock * h, n = sc.live ? lim - slot0 : 0;   // slots of the page that the row sees
-                    const float lv = sc.lv;
-                    const bool border = !sc.live || slot0 + kBlock > lim0;    // (lim0: the same for the row tile)
-                    float c = qs * sc.ks, slack = kPfSlack;
-                    if (primed && !border && !far && !sc.odd) {
-                        // Every row has a reference, and most pages do not exceed it: their weights are taken at once.  A
-                        // sum that f16 holds says that none of them left its range; else the page is done again below.
-                        // (c may be infinite here: scores that are not below zero leave the range then.)
+                    for (int h = 0; h < HALVES; ++h) {
+                        const uint32_t tS = lanes + (uint32_t)((SB * i + it % SB) * BN + kBlock * h);
+                        const PfScale& sc = hdr->sc[it % kPfRing][h];
+                        const int slot0 = u * BN + kBlock * h, n = sc.live ? lim - slot0 : 0;   // slots of the page that the row sees
+                        const float lv = sc.lv;
+                        const bool border = !sc.live || slot0 + kBlock > lim0;    // (lim0: the same for the row tile)
+                        float c = qs * sc.ks, slack = kPfSlack;
+                        if (primed && !border && !far && !sc.odd) {
+                            // Every row has a reference, and most pages do not exceed it: their weights are taken at once.  A
+                            // sum that f16 holds says that none of them left its range; else the page is done again below.
+                            // (c may be infinite here: scores that are not below zero leave the range then.)
+                            float s[kBlock];
+                            tm_ld32(tS, s);
+                            tm_ld32(tS + 32, s + 32);
+                            const float2 cc = make_float2(c, c), bb = make_float2(lv - mx, lv - mx);
+                            float2 add[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                            uint32_t w[SPLIT ? 1 : 32];
+                            auto weights = [&](int y) {
+#pragma unroll
+                                for (int x = y; x < y + 32; x += 2) {
+                                    const float2 e = fma2(make_float2(s[x], s[x + 1]), cc, bb);
+                                    s[x] = ex2(e.x);
+                                    s[x + 1] = ex2(e.y);
+                                    add[(x >> 1) & 1] = add2(add[(x >> 1) & 1], make_float2(s[x], s[x + 1]));
+                                    if constexpr (!SPLIT) w[x >> 1] = pack_f16(s[x], s[x + 1]);
+                                }
+                            };
+                            tm_wait32(s);
+                            tm_wait32(s + 32);
+                            weights(0);
+                            weights(32);
+                            const float sum = (add[0].x + add[0].y) + (add[1].x + add[1].y);
+                            if (__all_sync(0xffffffffu, sum <= 60000.0f)) {
+                                l = fmaf(sum, sc.iv, l);
+                                if constexpr (SPLIT) {
+                                    store_weights<SPLIT>(tS, s);
+                                } else {
+                                    tm_st16(tS, w);
+                                    tm_st16(tS + 16, w + 16);
+                                }
+                                tm_wait_st();
+                                tc_fence_before();
+                                mbar_arrive(&hdr->pready[i][h][it & 1]);
+                                continue;
+                            }
+                            slack = 0.0f;
+                        }
                         float s[kBlock];
                         tm_ld32(tS, s);
                         tm_ld32(tS + 32, s + 32);
-                        const float2 cc = make_float2(c, c), bb = make_float2(lv - mx, lv - mx);
-                        float2 add[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                        uint32_t w[SPLIT ? 1 : 32];
-                        auto weights = [&](int y) {
-#pragma unroll
-                            for (int x = y; x < y + 32; x += 2) {
-                                const float2 e = fma2(make_float2(s[x], s[x + 1]), cc, bb);
-                                s[x] = ex2(e.x);
-                                s[x + 1] = ex2(e.y);
-                                add[(x >> 1) & 1] = add2(add[(x >> 1) & 1], make_float2(s[x], s[x + 1]));
-                                if constexpr (!SPLIT) w[x >> 1] = pack_f16(s[x], s[x + 1]);
-                            }
-                        };
                         tm_wait32(s);
                         tm_wait32(s + 32);
-                        weights(0);
-                        weights(32);
-                        const float sum = (add[0].x + add[0].y) + (add[1].x + add[1].y);
-                        if (__all_sync(0xffffffffu, sum <= 60000.0f)) {
-                            l = fmaf(sum, sc.iv, l);
-                            if constexpr (SPLIT) {
-                                store_weights<SPLIT>(tS, s);
-                            } else {
-                                tm_st16(tS, w);
-                                tm_st16(tS + 16, w + 16);
-                            }
-                            tm_wait_st();
-                            tc_fence_before();
-                            mbar_arrive(&hdr->pready[i][h][it & 1]);
-                            continue;
-                        }
-                        slack = 0.0f;
-                    }
-                    float s[kBlock];
-                    tm_ld32(tS, s);
-                    tm_ld32(tS + 32, s + 32);
-                    tm_wait32(s);
-                    tm_wait32(s + 32);
-                    // an overflow of the factors' product is no score's (keys of zero score 0 whatever their scale): then one by one
-                    const bool huge = fabsf(c) == __uint_as_float(0x7f800000u);
-                    if (border || huge) {
-                        if (huge) c = qs;
+                        // an overflow of the factors' product is no score's (keys of zero score 0 whatever their scale): then one by one
+                        const bool huge = fabsf(c) == __uint_as_float(0x7f800000u);
+                        if (border || huge) {
+                            if (huge) c = qs;
 #pragma unroll 1
-                        for (int both = huge; both >= 0; --both) {
-                            const float a = both ? sc.ks : c;
+                            for (int both = huge; both >= 0; --both) {
+                                const float a = both ? sc.ks : c;
 #pragma unroll
-                            for (int x = 0; x < kBlock; ++x) s[x] = x < n ? s[x] * a : ninf;
-                        }
-                        c = 1.0f;
-                    }
-                    float top = ninf;
-                    if (c < 0.0f) {     // (the same for all rows: the signs of the scales)
-#pragma unroll
-                        for (int x = 0; x < kBlock; ++x) top = fmaxf(top, -s[x]);
-                    } else {
-                        float t[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                        for (int x = 4; x < kBlock - 4; x += 8) {
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) t[y] = max3(t[y], s[x + y], s[x + 4 + y]);
-                        }
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) t[y] = fmaxf(t[y], s[kBlock - 4 + y]);
-                        top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-                    }
-                    top = top * fabsf(c) + lv;
-                    top -= kPfTop;
-                    if (__any_sync(0xffffffffu, top > mx + slack)) {
-                        const float now = fmaxf(mx, top);
-                        const float f = now == ninf ? 1.0f : ex2(mx - now);
-                        mx = now;
-                        primed = __all_sync(0xffffffffu, mx != ninf);
-                        l *= f;
-                        far = __any_sync(0xffffffffu, far || (now != ninf && fabsf(now) >= kAtFar));
-                        if (u != u0 || h) {
-                            // O holds the pages before: the last one's product has to be there
-                            if (!(ok = h ? wait(&hdr->padone[i][it & 1], it >> 1)
-                                         : wait(&hdr->pvdone[i][(it - 1) & 1], (it - 1) >> 1))) {
-                                broke = true;
-                                break;
+                                for (int x = 0; x < kBlock; ++x) s[x] = x < n ? s[x] * a : ninf;
                             }
-                            tc_fence_after();
-                            if (__any_sync(0xffffffffu, f != 1.0f)) {
-#pragma unroll 1
-                                for (int c = 0; c < D; c += 16) {
-                                    float o[16];
-                                    tm_ld16(tO + c, o);
-                                    uint32_t w[16];
+                            c = 1.0f;
+                        }
+                        float top = ninf;
+                        if (c < 0.0f) {     // (the same for all rows: the signs of the scales)
 #pragma unroll
-                                    for (int x = 0; x < 16; ++x) w[x] = __float_as_uint(o[x] * f);
-                                    tm_st16(tO + c, w);
+                            for (int x = 0; x < kBlock; ++x) top = fmaxf(top, -s[x]);
+                        } else {
+                            float t[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                            for (int x = 4; x < kBlock - 4; x += 8) {
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) t[y] = max3(t[y], s[x + y], s[x + 4 + y]);
+                            }
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) t[y] = fmaxf(t[y], s[kBlock - 4 + y]);
+                            top = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+                        }
+                        top = top * fabsf(c) + lv;
+                        top -= kPfTop;
+                        if (__any_sync(0xffffffffu, top > mx + slack)) {
+                            const float now = fmaxf(mx, top);
+                            const float f = now == ninf ? 1.0f : ex2(mx - now);
+                            mx = now;
+                            primed = __all_sync(0xffffffffu, mx != ninf);
+                            l *= f;
+                            far = __any_sync(0xffffffffu, far || (now != ninf && fabsf(now) >= kAtFar));
+                            if (u != u0 || h) {
+                                // O holds the pages before: the last one's product has to be there
+                                if (!(ok = h ? wait(&hdr->padone[i][it & 1], it >> 1)
+                                             : wait(&hdr->pvdone[i][(it - 1) & 1], (it - 1) >> 1))) {
+                                    broke = true;
+                                    break;
+                                }
+                                tc_fence_after();
+                                if (__any_sync(0xffffffffu, f != 1.0f)) {
+#pragma unroll 1
+                                    for (int c = 0; c < D; c += 16) {
+                                        float o[16];
+                                        tm_ld16(tO + c, o);
+                                        uint32_t w[16];
+#pragma unroll
+                                        for (int x = 0; x < 16; ++x) w[x] = __float_as_uint(o[x] * f);
+                                        tm_st16(tO + c, w);
+                                    }
                                 }
                             }
                         }
-                    }
-                    const float ref = mx == ninf ? 0.0f : mx;
-                    float bias = lv - ref;
-                    if (far) {   // the exponents, rounded as the maximum was and bounded
+                        const float ref = mx == ninf ? 0.0f : mx;
+                        float bias = lv - ref;
+                        if (far) {   // the exponents, rounded as the maximum was and bounded
 #pragma unroll
-                        for (int x = 0; x < kBlock; ++x) {
-                            const float e = __fsub_rn(__fadd_rn(__fmul_rn(s[x], c), lv), ref);
-                            s[x] = e > kPfTop + kPfSlack ? kPfTop + kPfSlack : e;   // (NaN stays)
+                            for (int x = 0; x < kBlock; ++x) {
+                                const float e = __fsub_rn(__fadd_rn(__fmul_rn(s[x], c), lv), ref);
+                                s[x] = e > kPfTop + kPfSlack ? kPfTop + kPfSlack : e;   // (NaN stays)
+                            }
+                            c = 1.0f;
+                            bias = 0.0f;
                         }
-                        c = 1.0f;
-                        bias = 0.0f;
-                    }
-                    float2 add[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                    const float2 cc = make_float2(c, c), bb = make_float2(bias, bias);
+                        float2 add[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                        const float2 cc = make_float2(c, c), bb = make_float2(bias, bias);
 #pragma unroll
-                    for (int x = 0; x < kBlock; x += 2) {
-                        const float2 e = fma2(make_float2(s[x], s[x + 1]), cc, bb);
-                        s[x] = ex2(e.x);
-                        s[x + 1] = ex2(e.y);
-                        add[(x >> 1) & 1] = add2(add[(x >> 1) & 1], make_float2(s[x], s[x + 1]));
-                    }
-                    l = fmaf((add[0].x + add[0].y) + (add[1].x + add[1].y), sc.iv, l);
-                    if (sc.odd) {  // zero, negative, tiny, huge or NaN: the ratio of scale and power of two, for the
-                                   // slots that the row sees (0 x inf and 0 x NaN would reach the others)
-                        const float f = sc.ratio;
+                        for (int x = 0; x < kBlock; x += 2) {
+                            const float2 e = fma2(make_float2(s[x], s[x + 1]), cc, bb);
+                            s[x] = ex2(e.x);
+                            s[x + 1] = ex2(e.y);
+                            add[(x >> 1) & 1] = add2(add[(x >> 1) & 1], make_float2(s[x], s[x + 1]));
+                        }
+                        l = fmaf((add[0].x + add[0].y) + (add[1].x + add[1].y), sc.iv, l);
+                        if (sc.odd) {  // zero, negative, tiny, huge or NaN: the ratio of scale and power of two, for the
+                                       // slots that the row sees (0 x inf and 0 x NaN would reach the others)
+                            const float f = sc.ratio;
 #pragma unroll
-                        for (int x = 0; x < kBlock; ++x) s[x] = x < n ? s[x] * f : 0.0f;
+                            for (int x = 0; x < kBlock; ++x) s[x] = x < n ? s[x] * f : 0.0f;
+                        }
+                        store_weights<SPLIT>(tS, s);
+                        tm_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(&hdr->pready[i][h][it & 1]);
                     }
-                    store_weights<SPLIT>(tS, s);
-                    tm_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(&hdr->pready[i][h][it & 1]);
+                    if (broke) break;
                 }
-                if (broke) break;
+                if (!ok) break;
             }
             if (!ok) break;
 
