@@ -624,7 +624,7 @@ spin_status_t spin_kv_prefill(const spin_kv_config* cfg, const void* q, int64_t 
  * behind the context and slots without a page (BAD_PAGE) keep their weight.  decay: finite (0: the
  * weight from before is not read).
  * Scores have spin_kv_attend's precision (with many rows, a row whose largest query value is far below those of its
- * neighbours, by up to 2^8, keeps them to 2^-31 of its own largest).  Sums are fp32 in an order that depends on the sizes
+ * neighbours, by up to 2^8, keeps them to 2^-31 of its own largest), and lse counts as log2(e) lse rounded to fp32.  Sums are fp32 in an order that depends on the sizes
  * alone.  Checked on the device: as in spin_kv_prefill.
  * workspace: spin_kv_weigh_workspace_size bytes, as spin_kv_prefill's. */
 spin_status_t spin_kv_weigh_workspace_size(const spin_kv_config* cfg, int64_t n_tokens, int32_t max_new,

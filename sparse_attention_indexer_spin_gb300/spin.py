@@ -555,7 +555,8 @@ def rope_frequencies(rot_dim, theta=10000.0, scaling=None, factor=1.0, original=
 
 def rope_turns(frequencies, device=None):
     """Radians a position (float64, [pairs]) as spin_rope's turns: round(f / (2 pi) 2^64) modulo 2^64, an
-    int64 tensor that holds the 64 bits, on `device` (by default where the frequencies are, or cuda)."""
+    int64 tensor that holds the 64 bits, on `device` (by default where the frequencies are, or cuda).  Set-up, kept for a model:
+    exact arithmetic on the host (0.2 ms for 64 pairs), which waits for frequencies that are on the device."""
     f = torch.as_tensor(frequencies)
     if f.dtype is not torch.float64 or f.dim() != 1 or not bool(torch.isfinite(f).all()):
         raise SpinError(1, "frequencies must be a finite float64 tensor of one dimension")
